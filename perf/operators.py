@@ -348,7 +348,7 @@ def run(state):
         if c["dir"] == "forward":
             offsets, order, place = s["plan"]
             v.nerf_route_plan(s["ids"], c["experts"], offsets, order, place, workspace=s["ws"])
-            v.nerf_route_gather(s["x"], c["k"], offsets, order, s["rows"])
+            v.nerf_route_gather(s["x"], offsets, place, s["rows"])
             v.nerf_route_combine(s["y"], offsets, place, s["weights"], s["out"])
             return dict(offsets=offsets, order=order, place=place, rows=s["rows"], out=s["out"])
         v.nerf_route_combine_grad(s["dout"], s["y"], s["offsets"], s["place"], s["weights"], s["dy"], s["dw"])
