@@ -185,6 +185,8 @@ def prepare(case, seed):
         if own:
             s["loss"], s["lse_out"] = empty(n, dtype=torch.float32), empty(n, dtype=torch.float32)
             s["grad"] = empty(n, V) if case["dir"] != "loss" else None
+            import volume_rendering_amd as v
+            s["ws"] = empty(max(1, v.nerf_distill_workspace_size(n, V)), dtype=torch.uint8)
         return s
     k, E = case["k"], case["experts"]
     S = n * k
@@ -368,7 +370,7 @@ def run(state):
                                  row_scale=s["row_scale"])
         return dict(grad=s["grad"])
     v.nerf_distill_topk(s["logits"], s["t_logits"], s["t_ids"], c["temperature"], s["loss"], lse=s["lse_out"],
-                        grad=s["grad"], row_scale=s["row_scale"])
+                        grad=s["grad"], row_scale=s["row_scale"], workspace=s["ws"])
     out = dict(loss=s["loss"], lse=s["lse_out"])
     if c["dir"] == "both":
         out["grad"] = s["grad"]
