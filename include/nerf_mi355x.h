@@ -179,7 +179,9 @@ int nerf_abi_version(void);
  * bitset, 5 cell id outside the cell grid, 6 live-list entry or bucket slot
  * outside the workspace, 7 compaction entry outside a workgroup's LDS list,
  * 8 an inverse-CDF weight outside nerf_sample_pdf's precondition (finite, in
- * [0, 100]); all bits set: the flags could not be read. */
+ * [0, 100]), 9 routing slot, pair or sample row out of range, 10 expert
+ * offsets decreasing or past the slots; all bits set: the flags could not be
+ * read. */
 int64_t nerf_check_flags(void);
 const char* nerf_status_str(nerf_status s);
 /* Thread-local text of the last error on this thread ("" if none). */
@@ -468,6 +470,158 @@ nerf_status nerf_hash_inr_train_step(const float* x, const float* target, int64_
                                      const nerf_hash_inr_cfg* cfg, float* params, float* adam_m, float* adam_v,
                                      int64_t step, float* grad, float* loss, float* pred, void* workspace,
                                      size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------- */
+/* Routed fields: samples to experts and back (device)                    */
+/* ---------------------------------------------------------------------- */
+/*
+ * A routed field is a set of networks ("experts": one per cell, as in
+ * "KiloNeRF: Speeding up Neural Radiance Fields with Thousands of Tiny MLPs",
+ * or chosen by a gate) of which every sample uses up to k.  The calls below
+ * are its training and serving steps; the order of a pass is
+ *   nerf_route_plan -> nerf_route_gather -> nerf_expert_linear (per layer)
+ *   -> nerf_route_combine,
+ * and backwards
+ *   nerf_route_combine_grad -> nerf_expert_linear_grad (per layer)
+ *   -> nerf_route_combine with weights NULL (the gradient of the gather).
+ * The first layer can read the samples' rows through the plan (`order`)
+ * instead of gathered rows.  A "pair" p = t*k + j is choice j of sample t, a
+ * "slot" its place in expert order; slots 0 .. offsets[E]-1 belong to experts,
+ * the rest to pairs without one.
+ * Shared conventions: dtype is NERF_F32 or NERF_BF16 and is the type of every
+ * `const void*`/`void*` tensor of the call; sums are float32 and rounded once
+ * on output.  ld_* is the row stride in elements (0: contiguous); rows may
+ * start at any element (16-byte aligned rows are fastest).  Outputs must not
+ * overlap inputs.  offsets, order and place come from nerf_route_plan; entries
+ * out of range are skipped, never followed.  No call allocates when its
+ * workspace is given (or needs none), none uses atomics on its results: every
+ * result is the same from run to run.
+ */
+#define NERF_MAX_EXPERTS 4096
+#define NERF_MAX_CHOICES 64
+
+/* Device workspace of nerf_route_plan (0 for small inputs or invalid sizes). */
+size_t nerf_route_workspace_size(int64_t n, int k, int n_experts);
+
+/* Sorts the n*k pairs by expert, stably.  ids: device int32 [n, k], the expert
+ * of each pair; a value outside [0, n_experts) means no expert (dropped).
+ * offsets: device int32 [n_experts + 1], expert e owns slots offsets[e] ..
+ * offsets[e+1]-1 and offsets[n_experts] is the number of pairs with an expert;
+ * order: device int32 [n*k], the pair of each slot (dropped pairs last, in
+ * order); place: device int32 [n, k], the slot of each pair.  n == 0 writes
+ * offsets (zeros).  workspace: device, 16-byte aligned, at least
+ * nerf_route_workspace_size bytes, or NULL (allocated stream-ordered).
+ * Errors: null pointers, n < 0, k outside 1..64, n_experts < 1, n*k >= 2^31;
+ * NERF_ERR_UNSUPPORTED for n_experts > 4096; workspace too small. */
+nerf_status nerf_route_plan(const int32_t* ids, int64_t n, int k, int n_experts, int32_t* offsets, int32_t* order,
+                            int32_t* place, void* workspace, size_t workspace_bytes, void* stream);
+
+/* rows[place[t][j]] = x[t] for pairs with an expert; the other slots' rows are
+ * zero.  x: device [n, d] with row stride ld_x; rows: device [n*k, d].  Its
+ * gradient is nerf_route_combine of the rows' gradient with weights NULL.
+ * Errors: null pointers, bad dtype or sizes, 0 < ld_x < d, misalignment. */
+nerf_status nerf_route_gather(const void* x, int dtype, int64_t ld_x, int64_t n, int k, int d, int n_experts,
+                              const int32_t* offsets, const int32_t* place, void* rows, void* stream);
+
+/* out[t] = sum_j weights[t][j] * y[place[t][j]] over the pairs with an expert,
+ * j ascending (0 for a sample without any; what y and weights hold for the
+ * other pairs does not matter).  y: device [n*k, d]; weights: device float32
+ * [n, k] or NULL (all 1); out: device [n, d] with row stride ld_out. */
+nerf_status nerf_route_combine(const void* y, int dtype, int64_t n, int k, int d, int n_experts,
+                               const int32_t* offsets, const int32_t* place, const float* weights, void* out,
+                               int64_t ld_out, void* stream);
+
+/* Gradient of nerf_route_combine: dy[place[t][j]] = weights[t][j] * dout[t]
+ * and dweights[t][j] = <y[place[t][j]], dout[t]> for pairs with an expert, 0
+ * for the others.  dout: device [n, d] with row stride ld_dout; dy: device
+ * [n*k, d]; dweights: device float32 [n, k] or NULL. */
+nerf_status nerf_route_combine_grad(const void* dout, int64_t ld_dout, const void* y, int dtype, int64_t n, int k,
+                                    int d, int n_experts, const int32_t* offsets, const int32_t* place,
+                                    const float* weights, void* dy, float* dweights, void* stream);
+
+/* One linear layer per expert. */
+typedef struct {
+    int32_t dtype;             /* of x, weights, y, dz and dx; NERF_BF16 products accumulate in float32 */
+    int32_t n_experts;         /* 1..4096 */
+    int32_t d_in, d_out;       /* 1..65536 */
+    int32_t relu;              /* forward: y = max(y, 0) (a NaN stays); gradient: x is the output of
+                                  such a layer, dx is 0 where x <= 0 */
+    int32_t k;                 /* with order: pairs per sample (x row of slot s = order[s] / k) */
+    int64_t x_rows;            /* rows of x: slots without order, samples with it */
+    int64_t ld_x;              /* row stride of x (0: d_in) */
+    int64_t ld_y;              /* row stride of y, or of dz in the gradient (0: d_out) */
+} nerf_expert_layer;
+
+/* y[s] = act(W_e x[row(s)] + b_e) for the slots s of every expert e; rows of
+ * slots without an expert are zero.  x: device [x_rows, d_in]; weights: device
+ * [n_experts, d_out, d_in]; bias: device float32 [n_experts, d_out] or NULL;
+ * offsets, order: from nerf_route_plan, order NULL if x is in slot order;
+ * y: device [slots, d_out].  Errors: null pointers, bad dtype, sizes, strides
+ * or alignment, x_rows < slots without order. */
+nerf_status nerf_expert_linear(const nerf_expert_layer* layer, const void* x, const void* weights, const float* bias,
+                               const int32_t* offsets, const int32_t* order, int64_t slots, void* y, void* stream);
+
+/* Device workspace of nerf_expert_linear_grad's weight gradient (0: none). */
+size_t nerf_expert_linear_grad_workspace_size(int64_t slots, int n_experts, int d_in, int d_out);
+
+/* Gradients of z = W_e x + b_e per slot from dz (device [slots, d_out], the
+ * gradient at the layer's value before its activation):
+ *   dx[s] = W_e^T dz[s]          device [slots, d_in], or NULL; rows of slots without an expert
+ *                                are zero; times [x > 0] if layer->relu
+ *   dweights_e = sum_s dz[s] x[row(s)]^T   device float32 [n_experts, d_out, d_in], or NULL
+ *   dbias_e = sum_s dz[s]                  device float32 [n_experts, d_out], or NULL (needs dweights)
+ * Experts without slots get zeros.  Sums over slots are in a fixed order.
+ * With order, dx stays in slot order (nerf_route_combine with weights NULL sums
+ * it over a sample's pairs).  x may be NULL if dweights is NULL and relu is 0;
+ * weights if dx is NULL.  workspace: device, 16-byte aligned, or NULL
+ * (allocated stream-ordered).  Errors: as nerf_expert_linear, nothing asked
+ * for, dbias without dweights, workspace too small. */
+nerf_status nerf_expert_linear_grad(const nerf_expert_layer* layer, const void* dz, const void* x, const void* weights,
+                                    const int32_t* offsets, const int32_t* order, int64_t slots, void* dx,
+                                    float* dweights, float* dbias, void* workspace, size_t workspace_bytes,
+                                    void* stream);
+
+/* ---------------------------------------------------------------------- */
+/* Distillation from a teacher's top logits (device)                      */
+/* ---------------------------------------------------------------------- */
+/*
+ * For a head over many classes trained to follow a teacher of which only each
+ * row's `top` largest logits are kept.  Per row, with T = temperature:
+ *   p_j = softmax over the row's entries of t_logits / T
+ *   q_v = softmax over all classes of logits / T,  lse = ln sum_v exp(logits_v / T)
+ *   loss = T^2 sum_j p_j (ln p_j - ln q_{t_ids_j})
+ *   grad_v = row_scale * T * (q_v sum_j p_j - sum_{j: t_ids_j = v} p_j)
+ * An entry whose id is outside [0, classes) does not exist (padding); a row
+ * without entries, or with only -inf among them, has loss and gradient 0.  A
+ * teacher logit of -inf has p = 0 and adds nothing, whatever the student's.  A
+ * student logit of -inf has q = 0 (loss +inf if an entry with p > 0 is there);
+ * a row of only -inf has q = 0 and lse -inf.  NaN or +inf logits make the
+ * row's loss and gradient NaN.  Ids that occur twice add their masses.
+ * logits: device [n, classes] of dtype with row stride ld_logits (0:
+ * contiguous); t_logits: device float32 [n, top]; t_ids: device int32 [n,
+ * top]; top 1..256; row_scale: device float32 [n] or NULL (1): the gradient of
+ * the total with respect to each row's loss (0 for rows left out).
+ */
+
+/* Device workspace of nerf_distill_topk (0: none; rows few and long need it). */
+size_t nerf_distill_workspace_size(int64_t n, int64_t classes);
+
+/* loss: device float32 [n]; lse: device float32 [n] or NULL; grad: device [n,
+ * classes] of dtype with row stride ld_grad, or NULL: the gradient in the same
+ * call (it must not overlap logits).  workspace: device, 16-byte aligned, or
+ * NULL (allocated stream-ordered if needed).  Errors: null pointers, bad dtype,
+ * sizes, strides or alignment, temperature not positive and finite, grad ==
+ * logits, workspace too small. */
+nerf_status nerf_distill_topk(const void* logits, int dtype, int64_t ld_logits, int64_t n, int64_t classes,
+                              const float* t_logits, const int32_t* t_ids, int top, float temperature,
+                              const float* row_scale, float* loss, float* lse, void* grad, int64_t ld_grad,
+                              void* workspace, size_t workspace_bytes, void* stream);
+
+/* The gradient alone, from the lse that nerf_distill_topk returned. */
+nerf_status nerf_distill_topk_grad(const void* logits, int dtype, int64_t ld_logits, int64_t n, int64_t classes,
+                                   const float* t_logits, const int32_t* t_ids, int top, float temperature,
+                                   const float* row_scale, const float* lse, void* grad, int64_t ld_grad,
+                                   void* stream);
 
 /* ---------------------------------------------------------------------- */
 /* For callers that cannot allocate                                       */

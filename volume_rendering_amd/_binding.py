@@ -28,7 +28,10 @@ EXPORTED = [
     "nerf_encode_hashgrid", "nerf_mlp", "nerf_composite", "nerf_sample_pdf", "nerf_render",
     "nerf_render_workspace_size", "nerf_render_noalloc", "nerf_render_poses", "nerf_train_param_count",
     "nerf_train_workspace_size", "nerf_train_step", "nerf_hash_inr_param_count", "nerf_hash_inr_workspace_size",
-    "nerf_hash_inr_train_step", "nerf_check_flags",
+    "nerf_hash_inr_train_step", "nerf_check_flags", "nerf_route_workspace_size", "nerf_route_plan",
+    "nerf_route_gather", "nerf_route_combine", "nerf_route_combine_grad", "nerf_expert_linear",
+    "nerf_expert_linear_grad_workspace_size", "nerf_expert_linear_grad", "nerf_distill_workspace_size",
+    "nerf_distill_topk", "nerf_distill_topk_grad",
 ]
 
 
@@ -74,6 +77,12 @@ class nerf_train_cfg(C.Structure):
                 ("weights", C.c_void_p)]
 
 
+class nerf_expert_layer(C.Structure):
+    _fields_ = [("dtype", C.c_int32), ("n_experts", C.c_int32), ("d_in", C.c_int32), ("d_out", C.c_int32),
+                ("relu", C.c_int32), ("k", C.c_int32), ("x_rows", C.c_int64), ("ld_x", C.c_int64),
+                ("ld_y", C.c_int64)]
+
+
 class nerf_hash_inr_cfg(C.Structure):
     _fields_ = [("hidden", C.c_int32), ("n_out", C.c_int32), ("lr", C.c_float), ("beta1", C.c_float),
                 ("beta2", C.c_float), ("eps", C.c_float)]
@@ -116,6 +125,17 @@ def lib():
             "nerf_hash_inr_workspace_size": (S, [C.POINTER(nerf_hashgrid), C.POINTER(nerf_hash_inr_cfg), I64]),
             "nerf_hash_inr_train_step": (I, [P, P, I64, C.POINTER(nerf_hashgrid), C.POINTER(nerf_hash_inr_cfg), P, P, P,
                                              I64, P, P, P, P, S, P]),
+            "nerf_route_workspace_size": (S, [I64, I, I]),
+            "nerf_route_plan": (I, [P, I64, I, I, P, P, P, P, S, P]),
+            "nerf_route_gather": (I, [P, I, I64, I64, I, I, I, P, P, P, P]),
+            "nerf_route_combine": (I, [P, I, I64, I, I, I, P, P, P, P, I64, P]),
+            "nerf_route_combine_grad": (I, [P, I64, P, I, I64, I, I, I, P, P, P, P, P, P]),
+            "nerf_expert_linear": (I, [C.POINTER(nerf_expert_layer), P, P, P, P, P, I64, P, P]),
+            "nerf_expert_linear_grad_workspace_size": (S, [I64, I, I, I]),
+            "nerf_expert_linear_grad": (I, [C.POINTER(nerf_expert_layer), P, P, P, P, P, I64, P, P, P, P, S, P]),
+            "nerf_distill_workspace_size": (S, [I64, I64]),
+            "nerf_distill_topk": (I, [P, I, I64, I64, I64, P, P, I, C.c_float, P, P, P, P, I64, P, S, P]),
+            "nerf_distill_topk_grad": (I, [P, I, I64, I64, I64, P, P, I, C.c_float, P, P, P, I64, P]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -303,3 +323,206 @@ def nerf_hash_inr_train_step(x, target, grid: nerf_hashgrid, cfg: nerf_hash_inr_
     _check(lib().nerf_hash_inr_train_step(_ptr(x), _ptr(target), x.shape[0], C.byref(grid), C.byref(cfg),
                                           _ptr(params), _ptr(adam_m), _ptr(adam_v), int(step), _ptr(grad),
                                           _ptr(loss), _ptr(pred), ws, wsb, _stream()), "nerf_hash_inr_train_step")
+
+
+# ----------------------------------------------------------------------------
+# Routed fields: samples to experts and back
+# ----------------------------------------------------------------------------
+
+def _tensor(t, what: str, dtype, shape, strided: bool = False) -> int:
+    """Device pointer of ``t`` (0 for None) after checking type, shape and
+    layout; ``strided``: a matrix whose rows may be further apart."""
+    if t is None:
+        return 0
+    if t.dtype != dtype:
+        raise NerfError(f"{what}: dtype {t.dtype}, expected {dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise NerfError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_cuda:
+        raise NerfError(f"{what}: not a device tensor")
+    if not t.is_contiguous() and not (strided and t.dim() == 2 and (t.shape[1] == 1 or t.stride(1) == 1)
+                                      and (t.shape[0] <= 1 or t.stride(0) >= t.shape[1])):
+        raise NerfError(f"{what}: {'rows' if strided else 'tensor'} must be contiguous")
+    return t.data_ptr()
+
+
+def _ld(t) -> int:
+    """Row stride of a matrix (0: contiguous)."""
+    return 0 if t is None or t.is_contiguous() else t.stride(0)
+
+
+def _dtype_of(t, what: str) -> int:
+    import torch
+    if t.dtype == torch.bfloat16:
+        return NERF_BF16
+    if t.dtype == torch.float32:
+        return NERF_F32
+    raise NerfError(f"{what}: dtype {t.dtype}, expected float32 or bfloat16")
+
+
+def _matrix(t, what: str):
+    if t.dim() != 2:
+        raise NerfError(f"{what}: {t.dim()} dimensions, expected 2")
+    return t.shape
+
+
+def _ws(workspace):
+    return (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+
+
+def nerf_route_workspace_size(n: int, k: int, n_experts: int) -> int:
+    return lib().nerf_route_workspace_size(n, k, n_experts)
+
+
+def nerf_route_plan(ids, n_experts: int, offsets, order, place, workspace=None):
+    """Sorts sample-expert pairs by expert: ``ids`` int32 [n, k] (a value
+    outside [0, n_experts): no expert); writes int32 ``offsets``
+    [n_experts + 1], ``order`` [n*k] and ``place`` [n, k]."""
+    import torch
+    n, k = _matrix(ids, "ids")
+    i32 = torch.int32
+    ws, wsb = _ws(workspace)
+    _check(lib().nerf_route_plan(_tensor(ids, "ids", i32, (n, k)), n, k, n_experts,
+                                 _tensor(offsets, "offsets", i32, (n_experts + 1,)),
+                                 _tensor(order, "order", i32, (n * k,)), _tensor(place, "place", i32, (n, k)), ws, wsb,
+                                 _stream()), "nerf_route_plan")
+
+
+def nerf_route_gather(x, offsets, place, rows):
+    """rows[place[t, j]] = x[t]: ``x`` [n, d] (rows may be strided), ``rows``
+    [n*k, d]; rows of slots without an expert are zero."""
+    import torch
+    n, k = _matrix(place, "place")
+    d = _matrix(x, "x")[1]
+    E, i32 = offsets.numel() - 1, torch.int32
+    _check(lib().nerf_route_gather(_tensor(x, "x", x.dtype, (n, d), True), _dtype_of(x, "x"), _ld(x), n, k, d, E,
+                                   _tensor(offsets, "offsets", i32, (E + 1,)), _tensor(place, "place", i32, (n, k)),
+                                   _tensor(rows, "rows", x.dtype, (n * k, d)), _stream()), "nerf_route_gather")
+
+
+def nerf_route_combine(y, offsets, place, weights, out):
+    """out[t] = sum_j weights[t, j] y[place[t, j]]: ``y`` [n*k, d], ``weights``
+    float32 [n, k] or None (all 1), ``out`` [n, d] (rows may be strided).  With
+    weights None it is the gradient of nerf_route_gather."""
+    import torch
+    n, k = _matrix(place, "place")
+    d = _matrix(y, "y")[1]
+    E, i32 = offsets.numel() - 1, torch.int32
+    _check(lib().nerf_route_combine(_tensor(y, "y", y.dtype, (n * k, d)), _dtype_of(y, "y"), n, k, d, E,
+                                    _tensor(offsets, "offsets", i32, (E + 1,)), _tensor(place, "place", i32, (n, k)),
+                                    _tensor(weights, "weights", torch.float32, (n, k)),
+                                    _tensor(out, "out", y.dtype, (n, d), True), _ld(out), _stream()),
+           "nerf_route_combine")
+
+
+def nerf_route_combine_grad(dout, y, offsets, place, weights, dy, dweights=None):
+    """Gradient of nerf_route_combine: ``dout`` [n, d] (rows may be strided),
+    ``dy`` [n*k, d], ``dweights`` float32 [n, k] or None."""
+    import torch
+    n, k = _matrix(place, "place")
+    d = _matrix(y, "y")[1]
+    E, i32, f32 = offsets.numel() - 1, torch.int32, torch.float32
+    _check(lib().nerf_route_combine_grad(_tensor(dout, "dout", y.dtype, (n, d), True), _ld(dout),
+                                         _tensor(y, "y", y.dtype, (n * k, d)), _dtype_of(y, "y"), n, k, d, E,
+                                         _tensor(offsets, "offsets", i32, (E + 1,)),
+                                         _tensor(place, "place", i32, (n, k)),
+                                         _tensor(weights, "weights", f32, (n, k)),
+                                         _tensor(dy, "dy", y.dtype, (n * k, d)),
+                                         _tensor(dweights, "dweights", f32, (n, k)), _stream()),
+           "nerf_route_combine_grad")
+
+
+def _expert_layer(x, weight, ld_y, order, k, relu):
+    if weight.dim() != 3:
+        raise NerfError(f"weight: {weight.dim()} dimensions, expected 3")
+    E, d_out, d_in = weight.shape
+    if x.dim() != 2 or x.shape[1] != d_in:
+        raise NerfError(f"x: shape {tuple(x.shape)}, expected [rows, {d_in}]")
+    return nerf_expert_layer(_dtype_of(weight, "weight"), E, d_in, d_out, int(relu), k if order is not None else 0,
+                             x.shape[0], _ld(x), ld_y)
+
+
+def nerf_expert_linear(x, weight, bias, offsets, y, order=None, k=1, relu=False):
+    """y[s] = act(W_e x[s] + b_e) per slot s of expert e: ``weight`` [E, d_out,
+    d_in], ``bias`` float32 [E, d_out] or None, ``y`` [slots, d_out]; ``x`` is
+    [slots, d_in], or the samples' [n, d_in] rows with the plan's ``order`` and
+    ``k``.  Rows of ``x`` and ``y`` may be strided."""
+    import torch
+    L = _expert_layer(x, weight, _ld(y), order, k, relu)
+    E, d_out, d_in = weight.shape
+    slots, i32, dt = _matrix(y, "y")[0], torch.int32, weight.dtype
+    _check(lib().nerf_expert_linear(C.byref(L), _tensor(x, "x", dt, x.shape, True),
+                                    _tensor(weight, "weight", dt, weight.shape),
+                                    _tensor(bias, "bias", torch.float32, (E, d_out)),
+                                    _tensor(offsets, "offsets", i32, (E + 1,)),
+                                    _tensor(order, "order", i32, (slots,)),
+                                    slots, _tensor(y, "y", dt, (slots, d_out), True), _stream()),
+           "nerf_expert_linear")
+
+
+def nerf_expert_linear_grad_workspace_size(slots: int, n_experts: int, d_in: int, d_out: int) -> int:
+    return lib().nerf_expert_linear_grad_workspace_size(slots, n_experts, d_in, d_out)
+
+
+def nerf_expert_linear_grad(dz, x, weight, offsets, dx=None, dweight=None, dbias=None, order=None, k=1, relu_x=False,
+                            workspace=None):
+    """Gradients of nerf_expert_linear from ``dz`` [slots, d_out] (at the value
+    before its activation): ``dx`` [slots, d_in] (zero where x <= 0 with
+    ``relu_x``), float32 ``dweight`` [E, d_out, d_in] and ``dbias`` [E, d_out],
+    each optional."""
+    import torch
+    L = _expert_layer(x, weight, _ld(dz), order, k, relu_x)
+    E, d_out, d_in = weight.shape
+    slots, i32, dt, f32 = _matrix(dz, "dz")[0], torch.int32, weight.dtype, torch.float32
+    ws, wsb = _ws(workspace)
+    _check(lib().nerf_expert_linear_grad(C.byref(L), _tensor(dz, "dz", dt, (slots, d_out), True),
+                                         _tensor(x, "x", dt, x.shape, True),
+                                         _tensor(weight, "weight", dt, weight.shape),
+                                         _tensor(offsets, "offsets", i32, (E + 1,)),
+                                         _tensor(order, "order", i32, (slots,)), slots,
+                                         _tensor(dx, "dx", dt, (slots, d_in)),
+                                         _tensor(dweight, "dweight", f32, weight.shape),
+                                         _tensor(dbias, "dbias", f32, (E, d_out)), ws, wsb, _stream()),
+           "nerf_expert_linear_grad")
+
+
+# ----------------------------------------------------------------------------
+# Distillation from a teacher's top logits
+# ----------------------------------------------------------------------------
+
+def _distill_args(logits, t_logits, t_ids, temperature, row_scale):
+    import torch
+    n, classes = _matrix(logits, "logits")
+    top = _matrix(t_ids, "t_ids")[1]
+    return (_tensor(logits, "logits", logits.dtype, (n, classes), True), _dtype_of(logits, "logits"), _ld(logits), n,
+            classes, _tensor(t_logits, "t_logits", torch.float32, (n, top)),
+            _tensor(t_ids, "t_ids", torch.int32, (n, top)), top, float(temperature),
+            _tensor(row_scale, "row_scale", torch.float32, (n,)))
+
+
+def nerf_distill_workspace_size(n: int, classes: int) -> int:
+    return lib().nerf_distill_workspace_size(n, classes)
+
+
+def nerf_distill_topk(logits, t_logits, t_ids, temperature, loss, lse=None, grad=None, row_scale=None,
+                      workspace=None):
+    """Per-row distillation ``loss`` (float32 [n]) of the student's ``logits``
+    [n, classes] against the teacher's largest: ``t_logits`` float32 and
+    ``t_ids`` int32 [n, top].  Optional outputs: ``lse`` float32 [n] and
+    ``grad`` [n, classes], scaled by ``row_scale`` (float32 [n])."""
+    import torch
+    args = _distill_args(logits, t_logits, t_ids, temperature, row_scale)
+    n, f32 = logits.shape[0], torch.float32
+    ws, wsb = _ws(workspace)
+    _check(lib().nerf_distill_topk(*args, _tensor(loss, "loss", f32, (n,)), _tensor(lse, "lse", f32, (n,)),
+                                   _tensor(grad, "grad", logits.dtype, logits.shape, True), _ld(grad), ws, wsb,
+                                   _stream()), "nerf_distill_topk")
+
+
+def nerf_distill_topk_grad(logits, t_logits, t_ids, temperature, lse, grad, row_scale=None):
+    """The gradient of nerf_distill_topk alone, from its ``lse``."""
+    import torch
+    args = _distill_args(logits, t_logits, t_ids, temperature, row_scale)
+    _check(lib().nerf_distill_topk_grad(*args, _tensor(lse, "lse", torch.float32, (logits.shape[0],)),
+                                        _tensor(grad, "grad", logits.dtype, logits.shape, True), _ld(grad),
+                                        _stream()), "nerf_distill_topk_grad")

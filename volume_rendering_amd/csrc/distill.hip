@@ -1,0 +1,368 @@
+// Distillation from a teacher's K largest logits for gfx950.  Per row, with
+// z = s / T the student's scaled logits and t_j the teacher's logit of class
+// i_j:
+//   p_j = softmax_j(t / T) over the row's entries,  q = softmax(z) over all classes
+//   loss = T^2 sum_j p_j (ln p_j - ln q_{i_j}),     ln q_v = z_v - lse,  lse = ln sum_v e^{z_v}
+//   d loss / d s_v = T (P q_v - sum_{j: i_j = v} p_j),   P = sum_j p_j
+// P is 1, or 0 for a row without entries (loss and gradient 0).  The student's
+// logits are read once for the running maximum and sum of e^(z - max), and
+// once more for the gradient; both are bound by memory.  An exponential is
+// 2^((s - m) c), c = log2(e) / T: subtracting the maximum before scaling keeps
+// the exponent's error relative to s - m, however large the logits are.
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+
+#include "common.hpp"
+#include "experts.hpp"
+#include "rowio.hpp"
+
+namespace nerf {
+
+namespace {
+
+constexpr float kLog2e = 1.44269504088896341f;
+
+// Running maximum m of logits and sum s of 2^((x - m) c).  m is -inf as long as
+// only -inf was seen, and then s is 0; a NaN (or +inf) logit makes s NaN.
+struct MaxSum {
+    float m, s;
+};
+
+// 2^((x - m) c); with m = -inf every x is -inf (0) or NaN (x - x keeps it).
+__device__ __forceinline__ float exp2_below(float x, float m, float c) {
+    return m == -INFINITY ? (x == -INFINITY ? 0.0f : x - x) : __builtin_amdgcn_exp2f((x - m) * c);
+}
+
+__device__ __forceinline__ MaxSum join(const MaxSum& a, const MaxSum& b, float c) {
+    MaxSum r;
+    r.m = fmaxf(a.m, b.m);
+    // a part that saw nothing, or only NaN, has m = -inf and keeps its sum
+    const float fa = a.m == r.m || a.m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f((a.m - r.m) * c);
+    const float fb = b.m == r.m || b.m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f((b.m - r.m) * c);
+    r.s = a.s * fa + b.s * fb;
+    return r;
+}
+
+template <int NT>
+__device__ __forceinline__ MaxSum block_join(MaxSum v, float c, MaxSum* scratch) {  // scratch: [NT / 64]
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) {
+        const MaxSum o{__shfl_xor(v.m, off, 64), __shfl_xor(v.s, off, 64)};
+        v = join(v, o, c);
+    }
+    if constexpr (NT > 64) {
+        if ((threadIdx.x & 63) == 0) scratch[threadIdx.x >> 6] = v;
+        __syncthreads();
+        v = scratch[0];
+#pragma unroll 4
+        for (int w = 1; w < NT / 64; ++w) v = join(v, scratch[w], c);
+        __syncthreads();
+    }
+    return v;
+}
+
+template <class T>
+__device__ __forceinline__ void add_piece(MaxSum& a, const typename RowIO<T>::Vec& v, int n, float c) {
+    float z[RowIO<T>::PER], m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < RowIO<T>::PER; ++i) {
+        z[i] = i < n ? RowIO<T>::get(v, i) : -INFINITY;
+        m = fmaxf(m, z[i]);
+    }
+    if (m > a.m) {
+        if (a.m != -INFINITY) a.s *= __builtin_amdgcn_exp2f((a.m - m) * c);
+        a.m = m;
+    }
+#pragma unroll
+    for (int i = 0; i < RowIO<T>::PER; ++i) a.s += exp2_below(z[i], a.m, c);
+}
+
+// Maximum and sum of classes [c0, c1) of a row, by NT threads.
+template <class T, int NT>
+__device__ __forceinline__ MaxSum scan_row(const T* row, int64_t c0, int64_t c1, float c, MaxSum* scratch) {
+    constexpr int PER = RowIO<T>::PER;
+    MaxSum a{-INFINITY, 0.0f};
+    int64_t v = c0 + (int64_t)threadIdx.x * PER;
+    for (; v + 3 * NT * PER + PER <= c1; v += 4 * NT * PER) {  // four loads in flight
+        typename RowIO<T>::Vec x[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) x[u] = RowIO<T>::load(row, v + (int64_t)u * NT * PER, c1);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) add_piece<T>(a, x[u], PER, c);
+    }
+    for (; v < c1; v += NT * PER) {
+        const int64_t left = c1 - v;
+        add_piece<T>(a, RowIO<T>::load(row, v, c1), left < PER ? (int)left : PER, c);
+    }
+    return block_join<NT>(a, c, scratch);
+}
+
+// ---------------------------------------------------------------------------
+// The teacher's side of a row, by the first wave of a workgroup (lane l holds
+// entries l, l + 64, ...).  Entries whose class is outside [0, classes) do not
+// exist; a row whose entries are all missing or -inf has p = 0.
+// ---------------------------------------------------------------------------
+constexpr int kTopPerLane = kDistillMaxTop / 64;
+
+struct Teacher {
+    int id[kTopPerLane];   // -1: no entry
+    float p[kTopPerLane];
+    float logp[kTopPerLane];
+    float total;           // P
+};
+
+__device__ __forceinline__ Teacher teacher_row(const DistillArgs& a, int64_t row, int lane) {
+    Teacher t;
+    float z[kTopPerLane], m = -INFINITY, nan = 0.0f;
+    const float inv_t = 1.0f / a.temperature;
+#pragma unroll
+    for (int u = 0; u < kTopPerLane; ++u) {
+        const int j = lane + 64 * u;
+        t.id[u] = j < a.top ? a.t_ids[row * a.top + j] : -1;
+        if ((unsigned)t.id[u] >= (uint64_t)a.classes) t.id[u] = -1;
+        z[u] = t.id[u] >= 0 ? a.t_logits[row * a.top + j] * inv_t : -INFINITY;
+        m = fmaxf(m, z[u]);
+        if (z[u] != z[u]) nan = z[u];
+    }
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
+    float s = nan;
+#pragma unroll
+    for (int u = 0; u < kTopPerLane; ++u) {
+        t.p[u] = m == -INFINITY ? 0.0f : expf(z[u] - m);
+        s += t.p[u];
+    }
+    s = wave_sum(s);
+    const float ls = logf(s);
+#pragma unroll
+    for (int u = 0; u < kTopPerLane; ++u) {
+        t.logp[u] = z[u] - m - ls;
+        if (s != s)
+            t.p[u] = t.id[u] >= 0 ? s : 0.0f;
+        else
+            t.p[u] = s > 0.0f ? t.p[u] / s : 0.0f;
+    }
+    t.total = s != s ? s : s > 0.0f ? 1.0f : 0.0f;
+    return t;
+}
+
+// Loss of a row from its log-sum-exp (natural), by one wave.
+template <class T>
+__device__ __forceinline__ float row_loss(const DistillArgs& a, const Teacher& t, const T* row, float lse) {
+    float sum = 0.0f;
+#pragma unroll
+    for (int u = 0; u < kTopPerLane; ++u)
+        if (t.id[u] >= 0 && t.p[u] != 0.0f) {
+            const float logq = lse == -INFINITY ? -INFINITY : (float)row[t.id[u]] / a.temperature - lse;
+            sum += t.p[u] * (t.logp[u] - logq);
+        }
+    return a.temperature * a.temperature * wave_sum(sum);
+}
+
+// The gradient at the teacher's classes: after the sweep over the row has
+// stored scale P q there, the entries' owners store scale (P q - p), with the
+// masses of entries of one class added up.  Classes outside [c0, c1) belong to
+// another workgroup.
+struct TopLds {
+    int id[kDistillMaxTop];
+    float p[kDistillMaxTop];
+    float total;
+};
+
+template <class T, int NT>
+__device__ __forceinline__ void patch_top(const DistillArgs& a, const TopLds& t, const T* row, T* grad, int64_t c0,
+                                          int64_t c1, float c, float m, float inv, float scale) {
+    for (int j = threadIdx.x; j < a.top; j += NT) {
+        const int id = t.id[j];
+        if (id < 0 || id < c0 || id >= c1) continue;
+        float p = 0.0f;
+        for (int i = 0; i < a.top; ++i) p += t.id[i] == id ? t.p[i] : 0.0f;
+        const float q = exp2_below((float)row[id], m, c) * inv;
+        grad[id] = (T)(scale * (t.total * q - p));
+    }
+}
+
+template <class T, int NT>
+__device__ __forceinline__ void write_grad(const DistillArgs& a, const TopLds& t, const T* row, T* grad, int64_t c0,
+                                           int64_t c1, float c, float m, float inv, float scale) {
+    constexpr int PER = RowIO<T>::PER;
+    const float f = scale * t.total * inv;
+    // a row without entries has gradient 0 whatever its logits
+    const bool none = t.total == 0.0f;
+    for (int64_t v = c0 + (int64_t)threadIdx.x * PER; v < c1; v += NT * PER) {
+        const typename RowIO<T>::Vec x = RowIO<T>::load(row, v, c1);
+        float g[PER];
+#pragma unroll
+        for (int i = 0; i < PER; ++i) g[i] = none ? 0.0f : f * exp2_below(RowIO<T>::get(x, i), m, c);
+        RowIO<T>::store(grad, v, c1, RowIO<T>::pack(g));
+    }
+    __syncthreads();
+    if (!none) patch_top<T, NT>(a, t, row, grad, c0, c1, c, m, inv, scale);
+}
+
+template <class T>
+__device__ __forceinline__ void keep_top(TopLds& l, const Teacher& t, int top, int lane) {
+#pragma unroll
+    for (int u = 0; u < kTopPerLane; ++u)
+        if (lane + 64 * u < top) {
+            l.id[lane + 64 * u] = t.id[u];
+            l.p[lane + 64 * u] = t.p[u];
+        }
+    if (lane == 0) l.total = t.total;
+}
+
+__device__ __forceinline__ float natural_lse(const MaxSum& v, float temperature) {
+    return v.m == -INFINITY ? (v.s == 0.0f ? -INFINITY : v.s) : v.m / temperature + logf(v.s);
+}
+
+// ---------------------------------------------------------------------------
+// One workgroup per row: loss, and the gradient if asked for.
+// ---------------------------------------------------------------------------
+template <class T, int NT>
+__global__ void __launch_bounds__(NT) k_distill_rows(DistillArgs a) {
+    __shared__ MaxSum scratch[NT / 64];
+    __shared__ TopLds top;
+    const int64_t r = blockIdx.x;
+    const T* row = (const T*)a.logits + r * a.ld;
+    const float c = kLog2e / a.temperature;
+    const int lane = threadIdx.x & 63;
+    const MaxSum v = scan_row<T, NT>(row, 0, a.classes, c, scratch);
+    if (threadIdx.x < 64) {
+        const Teacher t = teacher_row(a, r, lane);
+        const float lse = natural_lse(v, a.temperature), loss = row_loss<T>(a, t, row, lse);
+        if (lane == 0) {
+            a.loss[r] = loss;
+            if (a.lse) a.lse[r] = lse;
+        }
+        keep_top<T>(top, t, a.top, lane);
+    }
+    if (!a.grad) return;
+    __syncthreads();
+    const float scale = a.temperature * (a.row_scale ? a.row_scale[r] : 1.0f);
+    write_grad<T, NT>(a, top, row, (T*)a.grad + r * a.ld_grad, 0, a.classes, c, v.m,
+                      v.s == 0.0f ? 0.0f : 1.0f / v.s, scale);
+}
+
+// ---------------------------------------------------------------------------
+// Few rows: the classes of a row are split over `splits` workgroups, whose
+// maxima and sums are joined by whoever needs them, in the same order.
+// ---------------------------------------------------------------------------
+constexpr int kSplitThreads = 256;
+
+__device__ __forceinline__ void split_range(int64_t classes, int splits, int i, int64_t& c0, int64_t& c1) {
+    // whole 16-byte pieces of bfloat16, the widest piece in elements
+    const int64_t per = ((classes + splits - 1) / splits + 7) & ~(int64_t)7;
+    c0 = per * i < classes ? per * i : classes;
+    c1 = c0 + per < classes ? c0 + per : classes;
+}
+
+template <class T>
+__global__ void __launch_bounds__(kSplitThreads) k_distill_part(DistillArgs a, int splits) {
+    __shared__ MaxSum scratch[kSplitThreads / 64];
+    const int64_t r = blockIdx.x / splits;
+    const int i = blockIdx.x % splits;
+    int64_t c0, c1;
+    split_range(a.classes, splits, i, c0, c1);
+    const MaxSum v = scan_row<T, kSplitThreads>((const T*)a.logits + r * a.ld, c0, c1, kLog2e / a.temperature, scratch);
+    if (threadIdx.x == 0) {
+        a.part[2 * (r * splits + i)] = v.m;
+        a.part[2 * (r * splits + i) + 1] = v.s;
+    }
+}
+
+__device__ __forceinline__ MaxSum joined_parts(const DistillArgs& a, int64_t r, int splits, int lane) {
+    MaxSum v{-INFINITY, 0.0f};
+    for (int i = lane; i < splits; i += 64) {
+        const MaxSum o{a.part[2 * (r * splits + i)], a.part[2 * (r * splits + i) + 1]};
+        v = join(v, o, kLog2e / a.temperature);
+    }
+    return block_join<64>(v, kLog2e / a.temperature, nullptr);
+}
+
+// grid: [n][max(gsplits, 1)]; the first workgroup of a row writes its loss.
+template <class T>
+__global__ void __launch_bounds__(kSplitThreads) k_distill_join(DistillArgs a, int splits, int gsplits) {
+    __shared__ TopLds top;
+    __shared__ MaxSum all;
+    const int64_t r = blockIdx.x / gsplits;
+    const int i = blockIdx.x % gsplits, lane = threadIdx.x & 63;
+    const T* row = (const T*)a.logits + r * a.ld;
+    if (threadIdx.x < 64) {
+        const MaxSum v = joined_parts(a, r, splits, lane);
+        const Teacher t = teacher_row(a, r, lane);
+        if (i == 0) {
+            const float lse = natural_lse(v, a.temperature), loss = row_loss<T>(a, t, row, lse);
+            if (lane == 0) {
+                a.loss[r] = loss;
+                if (a.lse) a.lse[r] = lse;
+            }
+        }
+        if (lane == 0) all = v;
+        keep_top<T>(top, t, a.top, lane);
+    }
+    if (!a.grad) return;
+    __syncthreads();
+    int64_t c0, c1;
+    split_range(a.classes, gsplits, i, c0, c1);
+    const float scale = a.temperature * (a.row_scale ? a.row_scale[r] : 1.0f);
+    write_grad<T, kSplitThreads>(a, top, row, (T*)a.grad + r * a.ld_grad, c0, c1, kLog2e / a.temperature, all.m,
+                                 all.s == 0.0f ? 0.0f : 1.0f / all.s, scale);
+}
+
+// Gradient from a saved log-sum-exp: q = e^(z - lse).
+template <class T>
+__global__ void __launch_bounds__(kSplitThreads) k_distill_grad(DistillArgs a, int gsplits) {
+    __shared__ TopLds top;
+    const int64_t r = blockIdx.x / gsplits;
+    const int i = blockIdx.x % gsplits, lane = threadIdx.x & 63;
+    if (threadIdx.x < 64) keep_top<T>(top, teacher_row(a, r, lane), a.top, lane);
+    __syncthreads();
+    int64_t c0, c1;
+    split_range(a.classes, gsplits, i, c0, c1);
+    const float scale = a.temperature * (a.row_scale ? a.row_scale[r] : 1.0f);
+    write_grad<T, kSplitThreads>(a, top, (const T*)a.logits + r * a.ld, (T*)a.grad + r * a.ld_grad, c0, c1,
+                                 kLog2e / a.temperature, a.lse[r] * a.temperature, 1.0f, scale);
+}
+
+// Workgroups per row of a gradient sweep: ranges of 16384 classes.
+int grad_splits(int64_t classes) { return (int)((classes + 16383) / 16384); }
+
+template <class T>
+void run_distill(const DistillArgs& a, hipStream_t s) {
+    const int splits = distill_splits(a.n, a.classes);
+    if (splits > 1) {
+        k_distill_part<T><<<(unsigned)(a.n * splits), kSplitThreads, 0, s>>>(a, splits);
+        const int gs = a.grad ? splits : 1;
+        k_distill_join<T><<<(unsigned)(a.n * gs), kSplitThreads, 0, s>>>(a, splits, gs);
+    } else if (a.classes <= 2048) {
+        k_distill_rows<T, 64><<<(unsigned)a.n, 64, 0, s>>>(a);
+    } else {
+        k_distill_rows<T, 256><<<(unsigned)a.n, 256, 0, s>>>(a);
+    }
+}
+
+}  // namespace
+
+int distill_splits(int64_t n, int64_t classes) {
+    if (n >= 1024 || classes <= 4096) return 1;
+    const int64_t most = classes / 2048, want = (1024 + n - 1) / n;
+    return (int)(want < most ? want : most);
+}
+
+void launch_distill(bool bf16, const DistillArgs& a, hipStream_t s) {
+    if (bf16)
+        run_distill<__bf16>(a, s);
+    else
+        run_distill<float>(a, s);
+}
+
+void launch_distill_grad(bool bf16, const DistillArgs& a, hipStream_t s) {
+    const int gs = grad_splits(a.classes);
+    if (bf16)
+        k_distill_grad<__bf16><<<(unsigned)(a.n * gs), kSplitThreads, 0, s>>>(a, gs);
+    else
+        k_distill_grad<float><<<(unsigned)(a.n * gs), kSplitThreads, 0, s>>>(a, gs);
+}
+
+}  // namespace nerf
