@@ -37,8 +37,9 @@ DEVICE = [f"--offload-arch={ARCH}", "-Xclang", "-target-feature", "-Xclang", "-p
           "-mllvm", "-amdgpu-mfma-vgpr-form"]
 # sources built without the VGPR-form option: the INR step's kernels (whose
 # small MFMA accumulators may live in AGPRs) make that pass of this compiler
-# fail on the larger decoder shapes
-DEVICE_AGPR_FORM = {"hash_train.hip"}
+# fail on the larger decoder shapes; the experts' products hold 256 accumulators
+# a lane, which is all of the architectural VGPRs
+DEVICE_AGPR_FORM = {"hash_train.hip", "experts.hip"}
 
 
 def _compile(src: str, checked: bool = False) -> str:

@@ -17,6 +17,12 @@ namespace nerf {
 
 namespace {
 
+#ifndef NERF_RT
+#define NERF_RT 256, 256, 128, 64
+#endif
+#ifndef NERF_WT
+#define NERF_WT 256, 256, 128, 64
+#endif
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 // ---------------------------------------------------------------------------
@@ -68,7 +74,7 @@ __device__ __forceinline__ Group find_group(const ExpertArgs& a, int64_t v, int6
 __device__ __forceinline__ int64_t x_row(const ExpertArgs& a, int64_t s) {
     if (!a.order) return s < a.x_rows ? s : -1;
     const int p = a.order[s];
-    const int64_t t = (unsigned)p / (unsigned)a.k;
+    const int64_t t = (int64_t)(((uint64_t)(uint32_t)p * a.k_mul) >> a.k_shift);  // p / k
     NERF_DCHECK(p >= 0 && t < a.x_rows, kCheckRouteSlot);
     return p >= 0 && t < a.x_rows ? t : -1;
 }
@@ -78,8 +84,9 @@ __device__ __forceinline__ int64_t x_row(const ExpertArgs& a, int64_t s) {
 //  k contiguous: a row is 128 bytes, its eight 16-byte pieces XOR-swizzled by
 //    row, so that a read of 32 rows at one piece falls on distinct banks.
 //  k outermost (k-major): a row is the tile's width at one k; bfloat16 pieces
-//    are swizzled by k in pairs (the transposing read takes 32 bytes of four
-//    consecutive k).
+//    are swizzled by k in pairs: the transposing read takes 32 bytes of four
+//    consecutive k per 16 lanes, and of two neighbouring 32 bytes per 32 lanes,
+//    which fall on distinct banks whether it serves 16 or 32 lanes at a time.
 // Every fragment is 16 bytes a lane: lanes 0..31 and 32..63 take the two
 // 16-byte pieces of a 32-byte step of k for their row.  For float32 that
 // permutes k within a step, the same way for both operands.
@@ -97,18 +104,21 @@ struct Elt {
     };
 };
 
-__device__ __forceinline__ int swz_row(int row) { return row & 7; }
+template <int KB = kStepBytes>
+__device__ __forceinline__ int swz_row(int row) {
+    return KB == 128 ? row & 7 : ((row >> 1) ^ (row >> 3)) & 3;  // 64-byte rows: two share the 32 banks
+}
 template <class T, int C>
 __device__ __forceinline__ int swz_k(int k) {
-    return sizeof(T) == 2 ? ((k & 3) << 2) & (C / 8 - 1) & ~1 : 0;
+    return sizeof(T) == 2 ? (((k & 3) << 1) | ((k & 1) << 3)) & (C / 8 - 1) : 0;
 }
 
 // Fragment of k-contiguous rows: row (lane % 32) + r0, 32-byte step q.
-template <class T>
+template <class T, int KB = kStepBytes>
 __device__ __forceinline__ typename Elt<T>::Frag frag_rows(const char* tile, int r0, int q, int lane) {
     typename Elt<T>::Frag f;
     const int r = r0 + (lane & 31);
-    f.u = *reinterpret_cast<const u32x4*>(tile + r * kStepBytes + (((2 * q + (lane >> 5)) ^ swz_row(r)) << 4));
+    f.u = *reinterpret_cast<const u32x4*>(tile + r * KB + (((2 * q + (lane >> 5)) ^ swz_row<KB>(r)) << 4));
     return f;
 }
 
@@ -239,6 +249,66 @@ __device__ __forceinline__ void epilogue_block(char* st, const f32x16 (&acc)[WN 
     }
 }
 
+// Columns n0 .. n0 + BN - 1 of `rows` rows of y to zero.
+template <class T, int BN, int NT>
+__device__ __forceinline__ void zero_rows(T* y, int64_t ld, int rows, int64_t n0, int64_t N, int tid) {
+    constexpr int PIECES = BN / RowIO<T>::PER;
+    for (int u = tid; u < rows * PIECES; u += NT) {
+        const int64_t n = n0 + (u % PIECES) * RowIO<T>::PER;
+        if (n < N) RowIO<T>::store(y + (int64_t)(u / PIECES) * ld, n, N, RowIO<T>::zero());
+    }
+}
+
+// Accumulators start at the bias (0 without one, and past the last column).
+template <bool GRAD, int WM, int WN>
+__device__ __forceinline__ void rows_start(const ExpertArgs& a, int e, f32x16 (&acc)[WM / 32][WN / 32], int64_t nw,
+                                           int64_t N, int lane) {
+#pragma unroll
+    for (int i = 0; i < WN / 32; ++i) {
+        f32x16 b;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) b[r] = 0.0f;
+        if (!GRAD && a.bias) {
+            const float* bias = a.bias + (int64_t)e * N;
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const int64_t n = nw + 32 * i + 8 * (r / 4) + 4 * (lane >> 5) + r % 4;
+                b[r] = bias[n < N ? n : N - 1];
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < WM / 32; ++j) acc[j][i] = b;
+    }
+}
+
+// A wave's WM x WN block of y (ReLU) or dx (the mask of x), from row r0 of the
+// group's `rows` and column nw.  WHOLE: N is a multiple of a piece.
+template <class T, bool GRAD, int WM, int WN, bool WHOLE = false>
+__device__ __forceinline__ void rows_epilogue(const ExpertArgs& a, const Group& g, char* st,
+                                              const f32x16 (&acc)[WM / 32][WN / 32], T* y, int rows, int r0,
+                                              int64_t nw, int64_t N, int lane) {
+    const float floor = !GRAD && a.relu ? 0.0f : -INFINITY;
+#pragma unroll
+    for (int j = 0; j < WM / 32; ++j) {
+        epilogue_block<T, WN>(
+            st, acc[j], lane, [&](float v, int) { return v < floor ? floor : v; },  // (a NaN stays)
+            [&](int m, int n, typename RowIO<T>::Vec v) {
+                const int r = r0 + 32 * j + m;
+                if (r >= rows || nw + n >= N) return;
+                if (GRAD && a.relu) {
+                    const int64_t t = x_row(a, g.lo + r);
+                    const typename RowIO<T>::Vec x =
+                        t < 0 ? RowIO<T>::zero()
+                              : RowIO<T>::load((const T*)a.x + t * a.ld_x, nw + n, WHOLE ? INT64_MAX : N);
+#pragma unroll
+                    for (int e = 0; e < RowIO<T>::PER; ++e)
+                        if (!(RowIO<T>::get(x, e) > 0.0f)) v.e[e] = (T)0.0f;
+                }
+                RowIO<T>::store(y + (int64_t)r * a.ld_y, nw + n, WHOLE ? INT64_MAX : N, v);
+            });
+    }
+}
+
 // ---------------------------------------------------------------------------
 // Forward and input gradient: a workgroup owns BM slots of one expert and BN
 // columns.  GRAD: weights are read k-major (k = outputs), rows are dz.
@@ -267,11 +337,7 @@ __global__ void __launch_bounds__((RowsTile<T, GRAD, BM, BN, WM, WN>::NT))
     const int64_t K = GRAD ? a.d_out : a.d_in, N = GRAD ? a.d_in : a.d_out;
     T* const y = (T*)a.y + g.lo * a.ld_y;
     if (g.e == a.n_experts) {  // slots without an expert: zero rows
-        constexpr int PIECES = BN / RowIO<T>::PER;
-        for (int u = tid; u < rows * PIECES; u += NT)
-            if (n0 + (u % PIECES) * RowIO<T>::PER < N)
-                RowIO<T>::store(y + (int64_t)(u / PIECES) * a.ld_y, n0 + (u % PIECES) * RowIO<T>::PER, N,
-                                RowIO<T>::zero());
+        zero_rows<T, BN, NT>(y, a.ld_y, rows, n0, N, tid);
         return;
     }
     const T* const w = (const T*)a.w + (int64_t)g.e * a.d_in * a.d_out;
@@ -302,12 +368,7 @@ __global__ void __launch_bounds__((RowsTile<T, GRAD, BM, BN, WM, WN>::NT))
     };
 
     f32x16 acc[WM / 32][WN / 32];
-#pragma unroll
-    for (int j = 0; j < WM / 32; ++j)
-#pragma unroll
-        for (int i = 0; i < WN / 32; ++i)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) acc[j][i][r] = 0.0f;
+    rows_start<GRAD, WM, WN>(a, g.e, acc, n0 + wn * WN, N, lane);
 
     load(0);
     store(lds);
@@ -336,39 +397,272 @@ __global__ void __launch_bounds__((RowsTile<T, GRAD, BM, BN, WM, WN>::NT))
         buf ^= 1;
     }
 
-    char* st = lds + wave * epilogue_bytes<T, WN>();
-    const int64_t nw = n0 + wn * WN;
-    const float* bias = !GRAD && a.bias ? a.bias + (int64_t)g.e * N : nullptr;
+    rows_epilogue<T, GRAD, WM, WN>(a, g, lds + wave * epilogue_bytes<T, WN>(), acc, y, rows, wm * WM, n0 + wn * WN, N,
+                                   lane);
+}
+
+// ---------------------------------------------------------------------------
+// Direct copies global -> LDS (no registers): bfloat16 with every row 16-byte
+// aligned.  Each instruction fills 1 KB of LDS in lane order, so the swizzle
+// is in the source: a lane fetches the piece that belongs where it writes.
+// Pieces past the matrix get an offset out of the buffer's range, which copies
+// zeros.
+// ---------------------------------------------------------------------------
+constexpr int64_t kDirectBytes = ((int64_t)1 << 32) - 65536;  // extent one buffer resource may cover
+
+// Values that are the same in every lane, kept in scalar registers.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ uint64_t uniform(const void* p) {
+    const uint64_t v = reinterpret_cast<uint64_t>(p);
+    return (uint64_t)(uint32_t)uniform((int)(v >> 32)) << 32 | (uint32_t)uniform((int)v);
+}
+// base and bytes uniform; bytes as an unsigned number
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_of(uint64_t base, int bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(base), (short)0, bytes, kBufferWord3);
+}
+__device__ __forceinline__ void copy16(__amdgpu_buffer_rsrc_t r, char* dst, uint32_t off) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (void NERF_LDS_PTR)dst, 16, (int)off, 0, 0, 0);
+}
+// This wave's copies have arrived and its LDS reads are done; then all waves'.
+// (__syncthreads() would do the same with a wait for stores in flight.)
+__device__ __forceinline__ void wait_copies_barrier() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(7 << 4);  // vmcnt(0) lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+template <int R, int NT>
+struct CopyRows {  // R rows, k contiguous
+    static constexpr int Q = R * 8 / NT;
+    static_assert(R * 8 % NT == 0, "whole copies");
+    uint32_t off[Q];
+    uint32_t piece;  // byte of this lane's piece within a k-step (the same in every copy)
+    // row_off(r): byte offset of row r, or kBufferOutOfRange
+    template <class F>
+    __device__ __forceinline__ void init(F&& row_off, int wave, int lane) {
+        piece = ((lane & 7) ^ (lane >> 3)) << 4;
 #pragma unroll
-    for (int j = 0; j < WM / 32; ++j) {
-        epilogue_block<T, WN>(
-            st, acc[j], lane,
-            [&](float v, int n) {
-                if (GRAD) return v;
-                if (bias && nw + n < N) v += bias[nw + n];
-                return a.relu && v < 0.0f ? 0.0f : v;  // (a NaN stays)
-            },
-            [&](int m, int n, typename RowIO<T>::Vec v) {
-                const int r = wm * WM + 32 * j + m;
-                if (r >= rows || nw + n >= N) return;
-                if (GRAD && a.relu) {
-                    const int64_t t = x_row(a, g.lo + r);
-                    const typename RowIO<T>::Vec x =
-                        t < 0 ? RowIO<T>::zero() : RowIO<T>::load((const T*)a.x + t * a.ld_x, nw + n, N);
-#pragma unroll
-                    for (int e = 0; e < RowIO<T>::PER; ++e)
-                        if (!(RowIO<T>::get(x, e) > 0.0f)) v.e[e] = (T)0.0f;
-                }
-                RowIO<T>::store(y + (int64_t)r * a.ld_y, nw + n, N, v);
-            });
+        for (int q = 0; q < Q; ++q) {
+            const uint32_t o = row_off((wave * Q + q) * 8 + (lane >> 3));
+            off[q] = o == kBufferOutOfRange ? o : o + piece;
+        }
     }
+    // copy q of the k-step at byte kb of rows of `width` bytes
+    __device__ __forceinline__ void issue(int q, __amdgpu_buffer_rsrc_t rs, char* tile, uint32_t kb, uint32_t width,
+                                          int wave) const {
+        const bool ok = off[q] != kBufferOutOfRange && kb + piece < width;
+        copy16(rs, tile + (wave * Q + q) * 1024, ok ? off[q] + kb : kBufferOutOfRange);
+    }
+};
+
+template <int C, int NT>
+struct CopyCols {  // one k-step (64 rows) of a k-major matrix, C columns
+    static constexpr int P = C / 8, Q = 64 * P / NT;
+    static_assert(64 * P % NT == 0, "whole copies");
+    uint32_t off[Q];  // bytes from the step's first row and the tile's first column; or out of range
+    static __device__ __forceinline__ int k_of(int q, int wave, int lane) { return ((wave * Q + q) * 64 + lane) / P; }
+    static __device__ __forceinline__ int piece(int q, int wave, int lane) {
+        return (((wave * Q + q) * 64 + lane) % P) ^ swz_k<__bf16, C>(k_of(q, wave, lane));
+    }
+    // rows `pitch` bytes apart, `cols` columns of the tile inside the matrix
+    __device__ __forceinline__ void init(uint32_t pitch, int cols, int wave, int lane) {
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            const int c = piece(q, wave, lane);
+            off[q] = 8 * c < cols ? k_of(q, wave, lane) * pitch + 16 * c : kBufferOutOfRange;
+        }
+    }
+    // copy q of a step: rows past the matrix lie past the resource's end
+    __device__ __forceinline__ void issue(int q, __amdgpu_buffer_rsrc_t rs, char* tile, int wave) const {
+        copy16(rs, tile + (wave * Q + q) * 1024, off[q]);
+    }
+};
+
+// k-steps of a k-major matrix: `rows` rows `pitch` bytes apart from base on,
+// which is `c0` bytes into the first.
+struct ColsSource {
+    uint64_t base;
+    int pitch, c0, rows;
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t step(int t) const {
+        const int left = rows - 64 * t;
+        const int kl = left < 0 ? 0 : left < 64 ? left : 64;
+        const int bytes = kl * pitch - c0;
+        return rsrc_of(base + (uint64_t)(64 * (int64_t)t * pitch), bytes < 0 ? 0 : bytes);
+    }
+};
+
+// ---------------------------------------------------------------------------
+// The product loop over k-steps of 64, two LDS stages.  Within a step the
+// fragments of the next 16 k are read while the current ones multiply, a read
+// or a copy between each two matrix instructions.  In a step's last quarter
+// every wave has its fragments in registers, so after one barrier the stage is
+// free: the copies of the step after next start there and have a whole step's
+// multiplications (2 to 4 microseconds of latency are not there to spare: one
+// workgroup fills a CU) to arrive in.
+//   read_m(stage, j, q), read_n(stage, i, q): fragments;  copy(c, t): copy c of
+//   step t;  before(t): what step t's copies need;  extra(fm): further use
+//   of a quarter's fragments.
+// ---------------------------------------------------------------------------
+template <int NM, int NN, int COPIES, class RM, class RN, class CP, class BF, class EX>
+__device__ __forceinline__ void product_loop(f32x16 (&acc)[NM][NN], int nk, RM&& read_m, RN&& read_n, CP&& copy,
+                                             BF&& before, EX&& extra) {
+    using Frag = Elt<__bf16>::Frag;
+    if (nk <= 0) return;
+    Frag fm[2][NM], fn[2][NN];
+    before(0);
+#pragma unroll
+    for (int c = 0; c < COPIES; ++c) copy(c, 0);
+    before(1);
+    wait_copies_barrier();
+#pragma unroll
+    for (int c = 0; c < COPIES; ++c) copy(c, 1);
+#pragma unroll
+    for (int j = 0; j < NM; ++j) fm[0][j] = read_m(0, j, 0);
+#pragma unroll
+    for (int i = 0; i < NN; ++i) fn[0][i] = read_n(0, i, 0);
+    for (int t = 0; t < nk; ++t) {
+        const int stage = t & 1;
+        before(t + 2);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            if (q == 3) wait_copies_barrier();
+            const int rs = q == 3 ? stage ^ 1 : stage, rq = (q + 1) & 3;
+            constexpr int CPM = (COPIES + NM * NN - 1) / (NM * NN), RPM = (NM + NN + NM * NN - 1) / (NM * NN);
+#pragma unroll
+            for (int m = 0; m < NM * NN; ++m) {
+                // (past the last step, fragments are read that an earlier one
+                // left and not used, and copies are of zeros)
+#pragma unroll
+                for (int u = 0; u < RPM; ++u) {
+                    const int r = m * RPM + u;
+                    if (r < NM)
+                        fm[(q + 1) & 1][r] = read_m(rs, r, rq);
+                    else if (r < NM + NN)
+                        fn[(q + 1) & 1][r - NM] = read_n(rs, r - NM, rq);
+                }
+                if (q == 3)
+#pragma unroll
+                    for (int u = 0; u < CPM; ++u)
+                        if (m * CPM + u < COPIES) copy(m * CPM + u, t + 2);
+                mma<__bf16>(acc[m / NN][m % NN], fn[q & 1][m % NN], fm[q & 1][m / NN]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            extra(fm[q & 1]);
+        }
+    }
+    wait_copies_barrier();
+}
+
+// Workgroup -> tile for consecutive work on one XCD (workgroup b runs on XCD
+// b % 8): each XCD gets a contiguous eighth of the tiles, and walks them four
+// slot tiles at a time, so that what its L2 holds of rows and weights is used
+// by its neighbours.
+struct TileAt {
+    int64_t v;  // virtual slot tile
+    int nt;
+};
+constexpr int kGroupTiles = 4;
+__device__ __forceinline__ TileAt tile_at(int64_t b, int64_t blocks, int64_t v_tiles, int n_tiles) {
+    const int64_t l = (b & 7) * (blocks >> 3) + (b >> 3);
+    const int64_t group = l / (kGroupTiles * n_tiles), in = l % (kGroupTiles * n_tiles);
+    const int64_t left = v_tiles - group * kGroupTiles;
+    const int wide = (int)(left < kGroupTiles ? left : kGroupTiles);
+    if (wide <= 0) return TileAt{-1, 0};
+    return TileAt{group * kGroupTiles + in % wide, (int)(in / wide)};
+}
+
+template <int BM, int BN, int WM, int WN, class O>
+struct DirectTile {
+    static constexpr int NT = 64 * (BM / WM) * (BN / WN);
+    static constexpr int A_BYTES = BM * kStepBytes, STAGE = A_BYTES + BN * kStepBytes;
+    static constexpr int EPI = (NT / 64) * epilogue_bytes<O, WN>();
+    static constexpr int LDS = 2 * STAGE > EPI ? 2 * STAGE : EPI;
+    static constexpr int QA = BM * 8 / NT, QB = BN * 8 / NT;  // copies of each operand per wave and step
+};
+
+template <bool GRAD, int BM, int BN, int WM, int WN>
+__global__ void __launch_bounds__((DirectTile<BM, BN, WM, WN, __bf16>::NT))
+    k_expert_rows_direct(ExpertArgs a, int64_t v_tiles, int n_tiles) {
+    using T = __bf16;
+    using L = DirectTile<BM, BN, WM, WN, T>;
+    constexpr int NT = L::NT;
+    __shared__ __attribute__((aligned(1024))) char lds[L::LDS];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave % (BM / WM), wn = wave / (BM / WM);
+    const TileAt at = tile_at(blockIdx.x, gridDim.x, v_tiles, n_tiles);
+    if (at.v < 0 || at.nt >= n_tiles) return;
+    const Group g = find_group(a, at.v, BM, a.n_experts + 1);
+    const int rows = (int)(g.hi - g.lo);
+    if (rows <= 0) return;
+    const int64_t n0 = (int64_t)at.nt * BN;
+    const int64_t K = GRAD ? a.d_out : a.d_in, N = GRAD ? a.d_in : a.d_out;
+    T* const y = (T*)a.y + g.lo * a.ld_y;
+    if (g.e == a.n_experts) {
+        zero_rows<T, BN, NT>(y, a.ld_y, rows, n0, N, tid);
+        return;
+    }
+    const T* const w = (const T*)a.w + (int64_t)g.e * a.d_in * a.d_out;
+    const uint32_t width = (uint32_t)(K * 2);
+    const int n_left = (int)(N - n0 < BN ? N - n0 : BN);
+
+    const bool through = !GRAD && a.order;
+    const int64_t lda = GRAD ? a.ld_dz : a.ld_x;
+    const T* const abase = GRAD ? (const T*)a.dz + g.lo * lda : through ? (const T*)a.x : (const T*)a.x + g.lo * lda;
+    const __amdgpu_buffer_rsrc_t ra =
+        rsrc_of(uniform(abase), uniform((int)(uint32_t)(((through ? a.x_rows : rows) - 1) * lda * 2 + K * 2)));
+    CopyRows<BM, NT> ca;
+    ca.init(
+        [&](int r) -> uint32_t {
+            if (r >= rows) return kBufferOutOfRange;
+            if (!through) return (uint32_t)(r * lda * 2);
+            const int64_t t = x_row(a, g.lo + r);
+            return t < 0 ? kBufferOutOfRange : (uint32_t)(t * lda * 2);
+        },
+        wave, lane);
+    // forward: rows of W; gradient: its columns
+    CopyRows<BN, NT> cb;
+    CopyCols<BN, NT> cc;
+    const __amdgpu_buffer_rsrc_t rb = rsrc_of(uniform(w + n0 * K), uniform((int)(n_left * K * 2)));
+    const ColsSource wc{uniform(w + n0), (int)(N * 2), (int)(n0 * 2), (int)K};
+    if (GRAD)
+        cc.init((uint32_t)(N * 2), n_left, wave, lane);
+    else
+        cb.init([&](int r) { return r < n_left ? (uint32_t)(r * K * 2) : kBufferOutOfRange; }, wave, lane);
+
+    f32x16 acc[WM / 32][WN / 32];
+    rows_start<GRAD, WM, WN>(a, g.e, acc, n0 + wn * WN, N, lane);
+    auto stage_at = [&](int st) { return lds + st * L::STAGE; };
+    __amdgpu_buffer_rsrc_t rk = rb;
+    product_loop<WM / 32, WN / 32, L::QA + L::QB>(
+        acc, (int)((K + 63) / 64),
+        [&](int st, int j, int q) { return frag_rows<T>(stage_at(st), wm * WM + 32 * j, q, lane); },
+        [&](int st, int i, int q) {
+            const char* tb = stage_at(st) + L::A_BYTES;
+            return GRAD ? frag_cols<T, BN>(tb, wn * WN + 32 * i, q, lane)
+                        : frag_rows<T>(tb, wn * WN + 32 * i, q, lane);
+        },
+        [&](int c, int t) {
+            char* slot = stage_at(t & 1);
+            if (c < L::QA)
+                ca.issue(c, ra, slot, (uint32_t)t * kStepBytes, width, wave);
+            else if constexpr (!GRAD)
+                cb.issue(c - L::QA, rb, slot + L::A_BYTES, (uint32_t)t * kStepBytes, width, wave);
+            else
+                cc.issue(c - L::QA, rk, slot + L::A_BYTES, wave);
+        },
+        [&](int t) {
+            if (GRAD) rk = wc.step(t);
+        },
+        [](const Elt<T>::Frag (&)[WM / 32]) {});
+    rows_epilogue<T, GRAD, WM, WN, true>(a, g, lds + wave * epilogue_bytes<T, WN>(), acc, y, rows, wm * WM,
+                                         n0 + wn * WN, N, lane);
 }
 
 // ---------------------------------------------------------------------------
 // Weight gradient: k runs over an expert's slots, both operands are k-major.
 // A workgroup owns BM outputs x BN inputs of one expert and, with a.chunk,
 // one range of its slots (partial sums, added in order by k_expert_sum).
-// Bias gradients are one more product, with a column of ones.
 // ---------------------------------------------------------------------------
 template <class T, int BM, int BN, int WM, int WN>
 struct WeightTile {
@@ -378,6 +672,89 @@ struct WeightTile {
     static constexpr int LDS = 2 * STAGE > EPI ? 2 * STAGE : EPI;
 };
 
+// The expert with the v-th most slots, for up to 64 experts (v beyond): the
+// longest sums start first, so that none starts when the others are done.
+__device__ __forceinline__ int longest_first(const ExpertArgs& a, int v) {
+    if (a.n_experts > 64) return v;
+    const int lane = lane_id();
+    const int mine = lane < a.n_experts ? a.offsets[lane + 1] - a.offsets[lane] : INT32_MIN;
+    int rank = 0;
+    for (int e = 0; e < a.n_experts; ++e) {
+        const int o = __builtin_amdgcn_readlane(mine, e);
+        rank += o > mine || (o == mine && e < lane);
+    }
+    return __ffsll((unsigned long long)__ballot(lane < a.n_experts && rank == v)) - 1;
+}
+
+// One workgroup's share of the weight gradients.
+struct WeightWork {
+    Group g;
+    int64_t m0, n0;
+    float* out;   // [d_out][d_in]
+    float* bout;  // [d_out], or NULL
+    bool any;
+};
+__device__ __forceinline__ WeightWork weight_work(const ExpertArgs& a, int64_t b, int m_tiles, int n_tiles, int BM,
+                                                  int BN) {
+    WeightWork w;
+    const int tile = (int)(b % (m_tiles * n_tiles));
+    const int64_t v = b / (m_tiles * n_tiles), M = a.d_out, N = a.d_in;
+    w.m0 = (int64_t)(tile / n_tiles) * BM;
+    w.n0 = (int64_t)(tile % n_tiles) * BN;
+    if (a.chunk) {
+        w.g = find_group(a, v, a.chunk, a.n_experts);
+        w.any = w.g.hi > w.g.lo;
+    } else {  // (an expert without slots gets zeros)
+        w.g.e = longest_first(a, (int)v);
+        w.g.lo = clamp_slot(a.offsets[w.g.e], a.slots);
+        w.g.hi = clamp_slot(a.offsets[w.g.e + 1], a.slots);
+        w.any = true;
+    }
+    w.out = a.chunk ? a.part + v * M * N : a.dw + w.g.e * M * N;
+    w.bout = !a.db || w.n0 ? nullptr : a.chunk ? a.bpart + v * M : a.db + w.g.e * M;
+    return w;
+}
+
+// A wave's WM x WN block of the weight gradient, and the bias gradients of its rows.
+template <int WM, int WN>
+__device__ __forceinline__ void weights_epilogue(const ExpertArgs& a, const WeightWork& w, char* st,
+                                                 const f32x16 (&acc)[WM / 32][WN / 32], const float (&bsum)[WM / 32],
+                                                 int64_t mw, int64_t nw, bool with_bias, int lane) {
+    const int64_t M = a.d_out, N = a.d_in;
+#pragma unroll
+    for (int j = 0; j < WM / 32; ++j) {
+        if (with_bias) {
+            const float b = bsum[j] + __shfl_xor(bsum[j], 32, 64);
+            if (lane < 32 && mw + 32 * j + lane < M) w.bout[mw + 32 * j + lane] = b;
+        }
+        epilogue_block<float, WN>(
+            st, acc[j], lane, [](float x, int) { return x; },
+            [&](int m, int n, typename RowIO<float>::Vec x) {
+                const int64_t r = mw + 32 * j + m;
+                if (r < M && nw + n < N) RowIO<float>::store(w.out + r * N, nw + n, N, x);
+            });
+    }
+}
+
+template <int NM, int NN>
+__device__ __forceinline__ void clear(f32x16 (&acc)[NM][NN]) {
+#pragma unroll
+    for (int j = 0; j < NM; ++j)
+#pragma unroll
+        for (int i = 0; i < NN; ++i)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[j][i][r] = 0.0f;
+}
+
+// Bias gradients are sums of the same fragments: a lane adds up its k of column lane % 32.
+template <class T, int NM>
+__device__ __forceinline__ void add_bias(float (&bsum)[NM], const typename Elt<T>::Frag (&fm)[NM]) {
+#pragma unroll
+    for (int j = 0; j < NM; ++j)
+#pragma unroll
+        for (int e = 0; e < Elt<T>::PER; ++e) bsum[j] += (float)fm[j].e[e];
+}
+
 template <class T, int BM, int BN, int WM, int WN>
 __global__ void __launch_bounds__((WeightTile<T, BM, BN, WM, WN>::NT))
     k_expert_weights(ExpertArgs a, int m_tiles, int n_tiles) {
@@ -386,47 +763,27 @@ __global__ void __launch_bounds__((WeightTile<T, BM, BN, WM, WN>::NT))
     __shared__ __attribute__((aligned(1024))) char lds[L::LDS];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int wm = wave % (BM / WM), wn = wave / (BM / WM);
-    const int tile = blockIdx.x % (m_tiles * n_tiles);
-    const int64_t v = blockIdx.x / (m_tiles * n_tiles);
-    const int64_t M = a.d_out, N = a.d_in;
-    const int64_t m0 = (int64_t)(tile / n_tiles) * BM, n0 = (int64_t)(tile % n_tiles) * BN;
-    Group g;
-    if (a.chunk) {
-        g = find_group(a, v, a.chunk, a.n_experts);
-        if (g.hi <= g.lo) return;
-    } else {
-        g.e = (int)v;
-        g.lo = clamp_slot(a.offsets[v], a.slots);
-        g.hi = clamp_slot(a.offsets[v + 1], a.slots);
-    }
-    float* const out = a.chunk ? a.part + v * M * N : a.dw + g.e * M * N;
-    float* const bout = a.chunk ? a.bpart + v * M : a.db ? a.db + g.e * M : nullptr;
-    const bool ones_tile = a.db && n0 == 0 && wn == 0;
+    const WeightWork w = weight_work(a, blockIdx.x, m_tiles, n_tiles, BM, BN);
+    if (!w.any) return;
+    const Group g = w.g;
+    const bool with_bias = w.bout && wn == 0;
 
     StageCols<T, BM, NT> sa;
     StageCols<T, BN, NT> sb;
     auto load = [&](int64_t s0) {
-        sa.load([&](int k) { return s0 + k < g.hi ? (const T*)a.dz + (s0 + k) * a.ld_dz : nullptr; }, m0, M, tid);
+        sa.load([&](int k) { return s0 + k < g.hi ? (const T*)a.dz + (s0 + k) * a.ld_dz : nullptr; }, w.m0, a.d_out,
+                tid);
         sb.load(
             [&](int k) -> const T* {
                 if (s0 + k >= g.hi) return nullptr;
                 const int64_t t = x_row(a, s0 + k);
                 return t < 0 ? nullptr : (const T*)a.x + t * a.ld_x;
             },
-            n0, N, tid);
+            w.n0, a.d_in, tid);
     };
-    f32x16 acc[WM / 32][WN / 32], bacc[WM / 32];
-#pragma unroll
-    for (int j = 0; j < WM / 32; ++j)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-            bacc[j][r] = 0.0f;
-#pragma unroll
-            for (int i = 0; i < WN / 32; ++i) acc[j][i][r] = 0.0f;
-        }
-    typename Elt<T>::Frag ones;
-#pragma unroll
-    for (int e = 0; e < Elt<T>::PER; ++e) ones.e[e] = (T)1.0f;
+    f32x16 acc[WM / 32][WN / 32];
+    float bsum[WM / 32] = {};
+    clear(acc);
 
     if (g.lo < g.hi) {
         load(g.lo);
@@ -450,9 +807,7 @@ __global__ void __launch_bounds__((WeightTile<T, BM, BN, WM, WN>::NT))
             for (int j = 0; j < WM / 32; ++j)
 #pragma unroll
                 for (int i = 0; i < WN / 32; ++i) mma<T>(acc[j][i], fn[i], fm[j]);
-            if (ones_tile)
-#pragma unroll
-                for (int j = 0; j < WM / 32; ++j) mma<T>(bacc[j], ones, fm[j]);
+            if (with_bias) add_bias<T>(bsum, fm);
         }
         if (more) {
             char* next = lds + (buf ^ 1) * L::STAGE;
@@ -462,19 +817,73 @@ __global__ void __launch_bounds__((WeightTile<T, BM, BN, WM, WN>::NT))
         __syncthreads();
         buf ^= 1;
     }
+    weights_epilogue<WM, WN>(a, w, lds + wave * epilogue_bytes<float, WN>(), acc, bsum, w.m0 + wm * WM,
+                             w.n0 + wn * WN, with_bias, lane);
+}
 
-    char* st = lds + wave * epilogue_bytes<float, WN>();
-    const int64_t mw = m0 + wm * WM, nw = n0 + wn * WN;
+// The same with direct copies (bfloat16).  THROUGH: x rows through the order.
+template <bool THROUGH, int BM, int BN, int WM, int WN>
+__global__ void __launch_bounds__((DirectTile<BM, BN, WM, WN, float>::NT))
+    k_expert_weights_direct(ExpertArgs a, int m_tiles, int n_tiles) {
+    using T = __bf16;
+    using L = DirectTile<BM, BN, WM, WN, float>;
+    constexpr int NT = L::NT;
+    using CB = CopyCols<BN, NT>;
+    __shared__ __attribute__((aligned(1024))) char lds[L::LDS];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave % (BM / WM), wn = wave / (BM / WM);
+    const WeightWork w = weight_work(a, blockIdx.x, m_tiles, n_tiles, BM, BN);
+    if (!w.any) return;
+    const Group g = w.g;
+    const bool with_bias = w.bout && wn == 0;
+    const int rows = uniform((int)(g.hi > g.lo ? g.hi - g.lo : 0));
+    const int m_left = (int)(a.d_out - w.m0 < BM ? a.d_out - w.m0 : BM);
+    const int n_left = (int)(a.d_in - w.n0 < BN ? a.d_in - w.n0 : BN);
+
+    f32x16 acc[WM / 32][WN / 32];
+    float bsum[WM / 32] = {};
+    clear(acc);
+    const ColsSource zs{uniform((const T*)a.dz + g.lo * a.ld_dz + w.m0), (int)(a.ld_dz * 2), (int)(w.m0 * 2), rows};
+    const ColsSource xs{uniform((const T*)a.x + (THROUGH ? 0 : g.lo * a.ld_x) + w.n0), (int)(a.ld_x * 2),
+                        (int)(w.n0 * 2), rows};
+    const __amdgpu_buffer_rsrc_t all =  // through the order: every row of x
+        rsrc_of(xs.base, uniform((int)(uint32_t)(((a.x_rows - 1) * a.ld_x + a.d_in - w.n0) * 2)));
+    CopyCols<BM, NT> ca;
+    CB cb;
+    ca.init((uint32_t)zs.pitch, m_left, wave, lane);
+    cb.init((uint32_t)xs.pitch, n_left, wave, lane);
+    __amdgpu_buffer_rsrc_t rz = all, rx = all;
+    auto stage_at = [&](int st) { return lds + st * L::STAGE; };
+    product_loop<WM / 32, WN / 32, L::QA + L::QB>(
+        acc, (rows + 63) / 64,
+        [&](int st, int j, int q) { return frag_cols<T, BM>(stage_at(st), wm * WM + 32 * j, q, lane); },
+        [&](int st, int i, int q) { return frag_cols<T, BN>(stage_at(st) + L::A_BYTES, wn * WN + 32 * i, q, lane); },
+        [&](int c, int t) {
+            char* slot = stage_at(t & 1);
+            if (c < L::QA)
+                ca.issue(c, rz, slot, wave);
+            else
+                cb.issue(c - L::QA, rx, slot + L::A_BYTES, wave);
+        },
+        [&](int t) {
+            rz = zs.step(t);
+            if constexpr (THROUGH) {
 #pragma unroll
-    for (int j = 0; j < WM / 32; ++j) {
-        if (ones_tile && lane < 32 && mw + 32 * j + lane < M) bout[mw + 32 * j + lane] = bacc[j][0];
-        epilogue_block<float, WN>(
-            st, acc[j], lane, [](float x, int) { return x; },
-            [&](int m, int n, typename RowIO<float>::Vec x) {
-                const int64_t r = mw + 32 * j + m;
-                if (r < M && nw + n < N) RowIO<float>::store(out + r * N, nw + n, N, x);
-            });
-    }
+                for (int q = 0; q < CB::Q; ++q) {
+                    const int64_t s = g.lo + 64 * (int64_t)t + CB::k_of(q, wave, lane);
+                    const int64_t r = s < g.hi ? x_row(a, s) : -1;
+                    const int c = CB::piece(q, wave, lane);
+                    cb.off[q] = r >= 0 && 8 * c < n_left ? (uint32_t)(r * a.ld_x * 2) + 16 * c : kBufferOutOfRange;
+                }
+            } else {
+                rx = xs.step(t);
+            }
+        },
+        [&](const Elt<T>::Frag (&fm)[WM / 32]) {
+            if (with_bias) add_bias<T>(bsum, fm);
+        });
+    weights_epilogue<WM, WN>(a, w, lds + wave * epilogue_bytes<float, WN>(), acc, bsum, w.m0 + wm * WM,
+                             w.n0 + wn * WN, with_bias, lane);
 }
 
 // dW_e (and db_e) from the partial sums of its ranges, in their order.
@@ -506,11 +915,35 @@ void run_rows(const ExpertArgs& a, hipStream_t s) {
         <<<(unsigned)(tiles * n_tiles), RowsTile<T, GRAD, BM, BN, WM, WN>::NT, 0, s>>>(a, n_tiles);
 }
 
+template <bool GRAD, int BM, int BN, int WM, int WN>
+void run_rows_direct(const ExpertArgs& a, hipStream_t s) {
+    const int64_t N = GRAD ? a.d_in : a.d_out;
+    const int n_tiles = (int)((N + BN - 1) / BN);
+    const int64_t v_tiles = a.slots / BM + a.n_experts + 1;
+    const int64_t blocks = (v_tiles * n_tiles + 7) / 8 * 8;
+    k_expert_rows_direct<GRAD, BM, BN, WM, WN>
+        <<<(unsigned)blocks, DirectTile<BM, BN, WM, WN, __bf16>::NT, 0, s>>>(a, v_tiles, n_tiles);
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// Whether the rows kernels may copy directly: bfloat16 rows of whole 16-byte
+// pieces, and a gathered x within one buffer resource.
+bool direct_rows(const ExpertArgs& a, bool grad) {
+    if (a.d_in % 8 || a.d_out % 8 || !aligned16(a.w)) return false;
+    const int64_t ld = grad ? a.ld_dz : a.ld_x;
+    if (ld % 8 || ld > 1 << 22) return false;  // (a tile of 256 such rows is within 2^31 bytes)
+    if (grad) return aligned16(a.dz);
+    return aligned16(a.x) && (!a.order || a.x_rows * a.ld_x * 2 < kDirectBytes);
+}
+
 template <class T, bool GRAD>
 void pick_rows(const ExpertArgs& a, hipStream_t s) {
     const int64_t N = GRAD ? a.d_in : a.d_out;
     if (a.slots / a.n_experts < 64 || N <= 32)
         run_rows<T, GRAD, 32, 32, 32, 32>(a, s);
+    else if (sizeof(T) == 2 && direct_rows(a, GRAD))
+        run_rows_direct<GRAD, NERF_RT>(a, s);
     else
         run_rows<T, GRAD, 128, 128, 64, 64>(a, s);
 }
@@ -523,10 +956,29 @@ void run_weights(const ExpertArgs& a, hipStream_t s) {
         <<<(unsigned)(items * mt * nt), WeightTile<T, BM, BN, WM, WN>::NT, 0, s>>>(a, mt, nt);
 }
 
+template <int BM, int BN, int WM, int WN>
+void run_weights_direct(const ExpertArgs& a, hipStream_t s) {
+    const int mt = (a.d_out + BM - 1) / BM, nt = (a.d_in + BN - 1) / BN;
+    const int64_t items = a.chunk ? a.slots / a.chunk + a.n_experts : a.n_experts;
+    constexpr int NT = DirectTile<BM, BN, WM, WN, float>::NT;
+    if (a.order)
+        k_expert_weights_direct<true, BM, BN, WM, WN><<<(unsigned)(items * mt * nt), NT, 0, s>>>(a, mt, nt);
+    else
+        k_expert_weights_direct<false, BM, BN, WM, WN><<<(unsigned)(items * mt * nt), NT, 0, s>>>(a, mt, nt);
+}
+
+// Whether the weight kernels may copy directly.
+bool direct_weights(const ExpertArgs& a) {
+    if (a.d_in % 8 || a.d_out % 8 || a.ld_x % 8 || a.ld_dz % 8 || a.ld_x > 1 << 22 || a.ld_dz > 1 << 22) return false;
+    return aligned16(a.x) && aligned16(a.dz) && (!a.order || a.x_rows * a.ld_x * 2 < kDirectBytes);
+}
+
 template <class T>
 void pick_weights(const ExpertArgs& a, hipStream_t s) {
     if (a.d_out <= 32 || a.d_in <= 32)
         run_weights<T, 32, 64, 32, 64>(a, s);
+    else if (sizeof(T) == 2 && direct_weights(a))
+        run_weights_direct<NERF_WT>(a, s);
     else
         run_weights<T, 128, 128, 64, 64>(a, s);
     if (a.chunk) {

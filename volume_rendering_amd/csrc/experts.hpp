@@ -59,7 +59,8 @@ struct ExpertArgs {
     int64_t slots;           // rows of y, dz and dx
     const int32_t* offsets;  // [n_experts + 1]
     const int32_t* order;    // [slots] pair of each slot (x row = pair / k), or NULL (x row = slot)
-    int k;
+    uint32_t k_mul;          // pair / k = (pair k_mul) >> k_shift for pairs below 2^31
+    int k_shift;
     int64_t x_rows;          // rows of x
     const void* x;
     int64_t ld_x;

@@ -98,8 +98,10 @@ nerf_status check_layer(const char* who, const nerf_expert_layer* L, const int32
                  "%s: widths %d -> %d outside 1..%d", who, L->d_in, L->d_out, kMaxWidth);
     NERF_REQUIRE(L->ld_x == 0 || L->ld_x >= L->d_in, "%s: ld_x %lld below d_in", who, (long long)L->ld_x);
     NERF_REQUIRE(L->ld_y == 0 || L->ld_y >= L->d_out, "%s: ld_y %lld below d_out", who, (long long)L->ld_y);
-    NERF_REQUIRE(slots >= 0 && slots <= kMaxPairs, "%s: slots %lld", who, (long long)slots);
-    NERF_REQUIRE(L->x_rows >= 0, "%s: x_rows %lld < 0", who, (long long)L->x_rows);
+    // (kernels count k-steps of 64 slots in 32 bits, two past the end)
+    NERF_REQUIRE(slots >= 0 && slots <= kMaxPairs - 255, "%s: slots %lld", who, (long long)slots);
+    NERF_REQUIRE(L->x_rows >= 0 && (L->x_rows > 0 || !order || slots == 0), "%s: x_rows %lld", who,
+                 (long long)L->x_rows);
     NERF_REQUIRE(!order || (L->k >= 1 && L->k <= NERF_MAX_CHOICES), "%s: k %d outside 1..%d", who, L->k,
                  NERF_MAX_CHOICES);
     if (L->n_experts > NERF_MAX_EXPERTS)
@@ -121,7 +123,12 @@ ExpertArgs expert_args(const nerf_expert_layer* L, const void* x, const void* w,
     a.slots = slots;
     a.offsets = offsets;
     a.order = order;
-    a.k = order ? L->k : 1;
+    // ceil(2^(31 + b) / k) with k <= 2^b: an exact quotient of 31-bit numbers
+    const uint32_t k = order ? (uint32_t)L->k : 1u;
+    int b = 0;
+    while ((1u << b) < k) ++b;
+    a.k_mul = (uint32_t)((((uint64_t)1 << (31 + b)) + k - 1) / k);
+    a.k_shift = 31 + b;
     a.x_rows = L->x_rows;
     a.x = x;
     a.ld_x = L->ld_x ? L->ld_x : L->d_in;
@@ -240,7 +247,7 @@ nerf_status nerf_expert_linear(const nerf_expert_layer* layer, const void* x, co
 }
 
 size_t nerf_expert_linear_grad_workspace_size(int64_t slots, int n_experts, int d_in, int d_out) {
-    if (slots < 0 || slots > kMaxPairs || n_experts < 1 || n_experts > NERF_MAX_EXPERTS || d_in < 1 ||
+    if (slots < 0 || slots > kMaxPairs - 255 || n_experts < 1 || n_experts > NERF_MAX_EXPERTS || d_in < 1 ||
         d_in > kMaxWidth || d_out < 1 || d_out > kMaxWidth)
         return 0;
     const int64_t chunk = expert_grad_chunk(slots, n_experts, d_in, d_out);
