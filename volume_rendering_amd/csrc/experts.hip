@@ -50,11 +50,13 @@ __device__ __forceinline__ int last_where(int n, F&& holds) {  // largest e < n 
 }
 
 struct Group {
-    int e;           // expert, or n_experts: the slots without one
-    int64_t lo, hi;  // its slots that this workgroup works on
+    int e;       // expert, or n_experts: the slots without one
+    int lo, hi;  // its slots that this workgroup works on
 };
 
-__device__ __forceinline__ int64_t clamp_slot(int64_t v, int64_t slots) { return v < 0 ? 0 : v > slots ? slots : v; }
+__device__ __forceinline__ int clamp_slot(int64_t v, int64_t slots) {
+    return v < 0 ? 0 : v > slots ? (int)slots : (int)v;
+}
 
 // Slots [lo, hi) of virtual tile v of B slots each; `groups` experts, the last
 // of which may be the slots without one.
@@ -70,19 +72,26 @@ __device__ __forceinline__ Group find_group(const ExpertArgs& a, int64_t v, int6
     return g;
 }
 
+// Row of x of pair p (-1: none).
+__device__ __forceinline__ int64_t row_of_pair(const ExpertArgs& a, int p) {
+    const int64_t t = (int64_t)(((uint64_t)(uint32_t)p * a.k_mul) >> a.k_shift);  // p / k
+    NERF_DCHECK(p < 0 || t < a.x_rows, kCheckRouteSlot);
+    return p >= 0 && t < a.x_rows ? t : -1;
+}
+
 // Row of x of slot s (-1: none).
 __device__ __forceinline__ int64_t x_row(const ExpertArgs& a, int64_t s) {
     if (!a.order) return s < a.x_rows ? s : -1;
     const int p = a.order[s];
-    const int64_t t = (int64_t)(((uint64_t)(uint32_t)p * a.k_mul) >> a.k_shift);  // p / k
-    NERF_DCHECK(p >= 0 && t < a.x_rows, kCheckRouteSlot);
-    return p >= 0 && t < a.x_rows ? t : -1;
+    NERF_DCHECK(p >= 0, kCheckRouteSlot);
+    return row_of_pair(a, p);
 }
 
 // ---------------------------------------------------------------------------
 // Tiles in LDS.  A k-step is 128 bytes of k (64 bfloat16 or 32 float32).
 //  k contiguous: a row is 128 bytes, its eight 16-byte pieces XOR-swizzled by
-//    row, so that a read of 32 rows at one piece falls on distinct banks.
+//    row, so that a read of 32 rows at one piece falls on distinct banks
+//    (whether 8 or 16 lanes are served at a time).
 //  k outermost (k-major): a row is the tile's width at one k; bfloat16 pieces
 //    are swizzled by k in pairs: the transposing read takes 32 bytes of four
 //    consecutive k per 16 lanes, and of two neighbouring 32 bytes per 32 lanes,
@@ -104,21 +113,18 @@ struct Elt {
     };
 };
 
-template <int KB = kStepBytes>
-__device__ __forceinline__ int swz_row(int row) {
-    return KB == 128 ? row & 7 : ((row >> 1) ^ (row >> 3)) & 3;  // 64-byte rows: two share the 32 banks
-}
+__device__ __forceinline__ int swz_row(int row) { return (row ^ (row >> 3)) & 7; }
 template <class T, int C>
 __device__ __forceinline__ int swz_k(int k) {
     return sizeof(T) == 2 ? (((k & 3) << 1) | ((k & 1) << 3)) & (C / 8 - 1) : 0;
 }
 
 // Fragment of k-contiguous rows: row (lane % 32) + r0, 32-byte step q.
-template <class T, int KB = kStepBytes>
+template <class T>
 __device__ __forceinline__ typename Elt<T>::Frag frag_rows(const char* tile, int r0, int q, int lane) {
     typename Elt<T>::Frag f;
     const int r = r0 + (lane & 31);
-    f.u = *reinterpret_cast<const u32x4*>(tile + r * KB + (((2 * q + (lane >> 5)) ^ swz_row<KB>(r)) << 4));
+    f.u = *reinterpret_cast<const u32x4*>(tile + r * kStepBytes + (((2 * q + (lane >> 5)) ^ swz_row(r)) << 4));
     return f;
 }
 
@@ -219,33 +225,33 @@ struct StageCols {  // one k-step of a k-major matrix, C columns
 // ---------------------------------------------------------------------------
 // A wave's accumulators to memory, through LDS so that rows leave in 16-byte
 // pieces along n.  One 32-row block of m at a time; `st` is the wave's own
-// 32 x (WN elements + 16 bytes).
+// 32 rows of WN elements, pieces swizzled by row (no padding: LDS is full).
 // ---------------------------------------------------------------------------
 template <class O, int WN>
-constexpr int epilogue_bytes() { return 32 * (WN * (int)sizeof(O) + 16); }
+constexpr int epilogue_bytes() { return 32 * WN * (int)sizeof(O); }
 
 template <class O, int WN, class V, class S>
 __device__ __forceinline__ void epilogue_block(char* st, const f32x16 (&acc)[WN / 32], int lane, V&& value, S&& store) {
-    constexpr int PITCH = WN * (int)sizeof(O) + 16, PER = 16 / (int)sizeof(O), PIECES = WN / PER;
+    constexpr int PER = 16 / (int)sizeof(O), PIECES = WN / PER, PITCH = PIECES * 16, MASK = PIECES < 8 ? PIECES - 1 : 7;
     wave_lds_sync();
 #pragma unroll
     for (int i = 0; i < WN / 32; ++i)
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-            const int n = 32 * i + 8 * g + 4 * (lane >> 5);
-            O* p = reinterpret_cast<O*>(st + (lane & 31) * PITCH) + n;
+            const int n = 32 * i + 8 * g + 4 * (lane >> 5), m = lane & 31;
+            char* p = st + m * PITCH + (((n / PER) ^ (m & MASK)) << 4) + (n % PER) * (int)sizeof(O);
             O o[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[e] = (O)value(acc[i][4 * g + e], n + e);
+            for (int e = 0; e < 4; ++e) o[e] = (O)value(acc[i][4 * g + e]);
             __builtin_memcpy(__builtin_assume_aligned(p, 4 * sizeof(O)), o, 4 * sizeof(O));
         }
     wave_lds_sync();
 #pragma unroll
-    for (int u = lane; u < 32 * PIECES; u += 64) {
-        const int m = u / PIECES, n = (u % PIECES) * PER;
+    for (int k = 0; k < PIECES / 2; ++k) {
+        const int u = 64 * k + lane, m = u / PIECES, c = u % PIECES;
         typename RowIO<O>::Vec v;
-        v.u = *reinterpret_cast<const u32x4*>(st + m * PITCH + n * (int)sizeof(O));
-        store(m, n, v);
+        v.u = *reinterpret_cast<const u32x4*>(st + m * PITCH + ((c ^ (m & MASK)) << 4));
+        store(m, c * PER, v);
     }
 }
 
@@ -291,7 +297,7 @@ __device__ __forceinline__ void rows_epilogue(const ExpertArgs& a, const Group& 
 #pragma unroll
     for (int j = 0; j < WM / 32; ++j) {
         epilogue_block<T, WN>(
-            st, acc[j], lane, [&](float v, int) { return v < floor ? floor : v; },  // (a NaN stays)
+            st, acc[j], lane, [&](float v) { return v < floor ? floor : v; },  // (a NaN stays)
             [&](int m, int n, typename RowIO<T>::Vec v) {
                 const int r = r0 + 32 * j + m;
                 if (r >= rows || nw + n >= N) return;
@@ -410,6 +416,13 @@ __global__ void __launch_bounds__((RowsTile<T, GRAD, BM, BN, WM, WN>::NT))
 // ---------------------------------------------------------------------------
 constexpr int64_t kDirectBytes = ((int64_t)1 << 32) - 65536;  // extent one buffer resource may cover
 
+// The same value, which the compiler takes for a new one: what depends on it is
+// computed where it is used, once a tile, and not kept in registers across the
+// loop over k.
+__device__ __forceinline__ int again(int v) {
+    asm volatile("" : "+v"(v));
+    return v;
+}
 // Values that are the same in every lane, kept in scalar registers.
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 __device__ __forceinline__ uint64_t uniform(const void* p) {
@@ -437,22 +450,29 @@ struct CopyRows {  // R rows, k contiguous
     static constexpr int Q = R * 8 / NT;
     static_assert(R * 8 % NT == 0, "whole copies");
     uint32_t off[Q];
-    uint32_t piece;  // byte of this lane's piece within a k-step (the same in every copy)
-    // row_off(r): byte offset of row r, or kBufferOutOfRange
+    static __device__ __forceinline__ int row(int q, int wave, int lane) { return (wave * Q + q) * 8 + (lane >> 3); }
+    // byte of a lane's piece within a k-step
+    static __device__ __forceinline__ uint32_t piece(int q, int wave, int lane) {
+        return (uint32_t)((lane & 7) ^ swz_row(row(q, wave, lane))) << 4;
+    }
+    uint32_t part;  // bit q: copy q's piece is inside the last, partial step
+    // row_off(q, r): byte offset of row r of `width` bytes, or kBufferOutOfRange
     template <class F>
-    __device__ __forceinline__ void init(F&& row_off, int wave, int lane) {
-        piece = ((lane & 7) ^ (lane >> 3)) << 4;
+    __device__ __forceinline__ void init(F&& row_off, uint32_t width, int wave, int lane) {
+        part = 0;
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
-            const uint32_t o = row_off((wave * Q + q) * 8 + (lane >> 3));
-            off[q] = o == kBufferOutOfRange ? o : o + piece;
+            const uint32_t o = row_off(q, row(q, wave, lane)), pc = piece(q, wave, lane);
+            off[q] = o == kBufferOutOfRange ? o : o + pc;
+            part |= (pc < width % kStepBytes ? 1u : 0u) << q;
         }
     }
-    // copy q of the k-step at byte kb of rows of `width` bytes
+    // copy q of the k-step at byte kb
     __device__ __forceinline__ void issue(int q, __amdgpu_buffer_rsrc_t rs, char* tile, uint32_t kb, uint32_t width,
                                           int wave) const {
-        const bool ok = off[q] != kBufferOutOfRange && kb + piece < width;
-        copy16(rs, tile + (wave * Q + q) * 1024, ok ? off[q] + kb : kBufferOutOfRange);
+        uint32_t o = __builtin_elementwise_add_sat(off[q], kb);  // (out of range stays so)
+        if (kb + kStepBytes > width) o = kb < width && (part >> q & 1) ? o : kBufferOutOfRange;
+        copy16(rs, tile + (wave * Q + q) * 1024, o);
     }
 };
 
@@ -488,175 +508,283 @@ struct ColsSource {
         const int left = rows - 64 * t;
         const int kl = left < 0 ? 0 : left < 64 ? left : 64;
         const int bytes = kl * pitch - c0;
-        return rsrc_of(base + (uint64_t)(64 * (int64_t)t * pitch), bytes < 0 ? 0 : bytes);
+        const uint64_t p = base + (uint64_t)(64 * (int64_t)t * pitch);
+        return rsrc_of(uniform(reinterpret_cast<const void*>(p)), uniform(bytes < 0 ? 0 : bytes));
     }
 };
 
 // ---------------------------------------------------------------------------
-// The product loop over k-steps of 64, two LDS stages.  Within a step the
-// fragments of the next 16 k are read while the current ones multiply, a read
+// One k-step of 64 of a product, in two LDS stages (an array for each stage of
+// each operand: the compiler then sees that reads need not wait for copies in
+// flight, which go into other arrays).
+// Fragments of the next 16 k are read while the current ones multiply, a read
 // or a copy between each two matrix instructions.  In a step's last quarter
 // every wave has its fragments in registers, so after one barrier the stage is
-// free: the copies of the step after next start there and have a whole step's
-// multiplications (2 to 4 microseconds of latency are not there to spare: one
-// workgroup fills a CU) to arrive in.
-//   read_m(stage, j, q), read_n(stage, i, q): fragments;  copy(c, t): copy c of
-//   step t;  before(t): what step t's copies need;  extra(fm): further use
-//   of a quarter's fragments.
+// free: the copies of the step after next start there, and have a step's
+// multiplications to arrive in.
+//   read(r, next, q, fm, fn): part r of NM + NN of the fragments of quarter q
+//   of this step or (next) of quarter 0 of the next one;
+//   ready(): a step's copies are about to start;  copy(c): copy c of them;
+//   extra(fm): further use of a quarter's fragments.
 // ---------------------------------------------------------------------------
-template <int NM, int NN, int COPIES, class RM, class RN, class CP, class BF, class EX>
-__device__ __forceinline__ void product_loop(f32x16 (&acc)[NM][NN], int nk, RM&& read_m, RN&& read_n, CP&& copy,
-                                             BF&& before, EX&& extra) {
-    using Frag = Elt<__bf16>::Frag;
-    if (nk <= 0) return;
-    Frag fm[2][NM], fn[2][NN];
-    before(0);
-#pragma unroll
-    for (int c = 0; c < COPIES; ++c) copy(c, 0);
-    before(1);
-    wait_copies_barrier();
-#pragma unroll
-    for (int c = 0; c < COPIES; ++c) copy(c, 1);
-#pragma unroll
-    for (int j = 0; j < NM; ++j) fm[0][j] = read_m(0, j, 0);
-#pragma unroll
-    for (int i = 0; i < NN; ++i) fn[0][i] = read_n(0, i, 0);
-    for (int t = 0; t < nk; ++t) {
-        const int stage = t & 1;
-        before(t + 2);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            if (q == 3) wait_copies_barrier();
-            const int rs = q == 3 ? stage ^ 1 : stage, rq = (q + 1) & 3;
-            constexpr int CPM = (COPIES + NM * NN - 1) / (NM * NN), RPM = (NM + NN + NM * NN - 1) / (NM * NN);
-#pragma unroll
-            for (int m = 0; m < NM * NN; ++m) {
-                // (past the last step, fragments are read that an earlier one
-                // left and not used, and copies are of zeros)
-#pragma unroll
-                for (int u = 0; u < RPM; ++u) {
-                    const int r = m * RPM + u;
-                    if (r < NM)
-                        fm[(q + 1) & 1][r] = read_m(rs, r, rq);
-                    else if (r < NM + NN)
-                        fn[(q + 1) & 1][r - NM] = read_n(rs, r - NM, rq);
-                }
-                if (q == 3)
-#pragma unroll
-                    for (int u = 0; u < CPM; ++u)
-                        if (m * CPM + u < COPIES) copy(m * CPM + u, t + 2);
-                mma<__bf16>(acc[m / NN][m % NN], fn[q & 1][m % NN], fm[q & 1][m / NN]);
-                __builtin_amdgcn_sched_barrier(0);
-            }
-            extra(fm[q & 1]);
-        }
-    }
-    wait_copies_barrier();
-}
-
-// Workgroup -> tile for consecutive work on one XCD (workgroup b runs on XCD
-// b % 8): each XCD gets a contiguous eighth of the tiles, and walks them four
-// slot tiles at a time, so that what its L2 holds of rows and weights is used
-// by its neighbours.
-struct TileAt {
-    int64_t v;  // virtual slot tile
-    int nt;
+template <int NM, int NN>
+struct Frags {
+    Elt<__bf16>::Frag m[2][NM], n[2][NN];
 };
-constexpr int kGroupTiles = 4;
-__device__ __forceinline__ TileAt tile_at(int64_t b, int64_t blocks, int64_t v_tiles, int n_tiles) {
-    const int64_t l = (b & 7) * (blocks >> 3) + (b >> 3);
-    const int64_t group = l / (kGroupTiles * n_tiles), in = l % (kGroupTiles * n_tiles);
-    const int64_t left = v_tiles - group * kGroupTiles;
-    const int wide = (int)(left < kGroupTiles ? left : kGroupTiles);
-    if (wide <= 0) return TileAt{-1, 0};
-    return TileAt{group * kGroupTiles + in % wide, (int)(in / wide)};
+
+template <int NM, int NN, int COPIES, class RD, class RY, class CP, class EX>
+__device__ __forceinline__ void product_step(f32x16 (&acc)[NM][NN], Frags<NM, NN>& f, RD&& read, RY&& ready, CP&& copy,
+                                             EX&& extra) {
+    constexpr int CPM = (COPIES + NM * NN - 1) / (NM * NN), RPM = (NM + NN + NM * NN - 1) / (NM * NN);
+    auto quarter = [&](auto qc) {
+        constexpr int q = decltype(qc)::value;
+        if constexpr (q == 3) {
+            wait_copies_barrier();
+            __builtin_amdgcn_sched_barrier(0);
+            ready();
+        }
+#pragma unroll
+        for (int m = 0; m < NM * NN; ++m) {
+#pragma unroll
+            for (int u = 0; u < RPM; ++u)
+                if (m * RPM + u < NM + NN)
+                    read(m * RPM + u, std::integral_constant<bool, q == 3>{}, (q + 1) & 3, f.m[(q + 1) & 1],
+                         f.n[(q + 1) & 1]);
+            if constexpr (q == 3)
+#pragma unroll
+                for (int u = 0; u < CPM; ++u)
+                    if (m * CPM + u < COPIES) copy(m * CPM + u);
+            mma<__bf16>(acc[m / NN][m % NN], f.n[q & 1][m % NN], f.m[q & 1][m / NN]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        extra(f.m[q & 1]);
+    };
+    quarter(std::integral_constant<int, 0>{});
+    quarter(std::integral_constant<int, 1>{});
+    quarter(std::integral_constant<int, 2>{});
+    quarter(std::integral_constant<int, 3>{});
 }
 
 template <int BM, int BN, int WM, int WN, class O>
 struct DirectTile {
     static constexpr int NT = 64 * (BM / WM) * (BN / WN);
-    static constexpr int A_BYTES = BM * kStepBytes, STAGE = A_BYTES + BN * kStepBytes;
+    static constexpr int A_BYTES = BM * kStepBytes, B_BYTES = BN * kStepBytes;  // a stage of each operand
     static constexpr int EPI = (NT / 64) * epilogue_bytes<O, WN>();
-    static constexpr int LDS = 2 * STAGE > EPI ? 2 * STAGE : EPI;
     static constexpr int QA = BM * 8 / NT, QB = BN * 8 / NT;  // copies of each operand per wave and step
+};
+
+// ---------------------------------------------------------------------------
+// The tiles of a rows product, dealt out to a grid that stays: workgroup b
+// runs on XCD b % 8, each XCD gets a contiguous eighth of the tiles, and its
+// workgroups walk it side by side, kGroupTiles slot tiles at a time, so that
+// what its L2 holds of rows and weights is used by its neighbours.  With up to
+// 63 experts the tiles are counted exactly (each lane holds an expert);
+// otherwise they are virtual tiles and the empty ones are skipped.
+// ---------------------------------------------------------------------------
+constexpr int kCus = 256;  // workgroups of a grid that stays: one per CU
+constexpr int kGroupTiles = 4;
+
+template <int BM>
+struct TileWalk {
+    int l, end, v_tiles, step, n_tiles;
+    int off, upto;  // lane e: first slot of expert e; tiles of experts 0 .. e
+
+    __device__ __forceinline__ void start(const ExpertArgs& a, int n) {
+        n_tiles = n;
+        const int groups = a.n_experts + 1;
+        if (groups <= 64) {
+            const int e = lane_id();
+            off = e < groups ? clamp_slot(a.offsets[e], a.slots) : (int)a.slots;
+            const int o1 = e < a.n_experts ? clamp_slot(a.offsets[e + 1], a.slots) : (int)a.slots;
+            upto = o1 > off ? (o1 - off + BM - 1) / BM : 0;
+#pragma unroll
+            for (int d = 1; d < 64; d <<= 1) {
+                const int o = __shfl_up(upto, d, 64);
+                if (e >= d) upto += o;
+            }
+            v_tiles = __builtin_amdgcn_readlane(upto, 63);
+        } else {
+            v_tiles = (int)(a.slots / BM) + groups;
+        }
+        const int part = blockIdx.x & 7;  // (fewer than 2^31 tiles: the host has checked)
+        l = (int)((int64_t)v_tiles * n_tiles * part / 8) + (int)(blockIdx.x >> 3);
+        end = (int)((int64_t)v_tiles * n_tiles * (part + 1) / 8);
+        step = gridDim.x >> 3;
+    }
+    // The next tile with slots; false: none is left.
+    __device__ __forceinline__ bool next(const ExpertArgs& a, Group& g, int& nt) {
+        while (l < end) {
+            const int group = (unsigned)l / (unsigned)(kGroupTiles * n_tiles), in = l - group * kGroupTiles * n_tiles;
+            const int left = v_tiles - group * kGroupTiles, wide = left < kGroupTiles ? left : kGroupTiles;
+            nt = (unsigned)in / (unsigned)wide;
+            const int v = group * kGroupTiles + in - nt * wide;
+            l += step;
+            if (a.n_experts + 1 <= 64) {
+                g.e = __popcll(__ballot(upto <= v));
+                const int before = g.e ? __builtin_amdgcn_readlane(upto, g.e - 1) : 0;
+                const int o1 = g.e < a.n_experts ? __builtin_amdgcn_readlane(off, g.e + 1) : (int)a.slots;
+                g.lo = __builtin_amdgcn_readlane(off, g.e) + (v - before) * BM;
+                g.hi = o1 - g.lo > BM ? g.lo + BM : o1;
+            } else {
+                g = find_group(a, v, BM, a.n_experts + 1);
+            }
+            if (g.lo < g.hi) return true;
+        }
+        return false;
+    }
 };
 
 template <bool GRAD, int BM, int BN, int WM, int WN>
 __global__ void __launch_bounds__((DirectTile<BM, BN, WM, WN, __bf16>::NT))
-    k_expert_rows_direct(ExpertArgs a, int64_t v_tiles, int n_tiles) {
+    k_expert_rows_direct(ExpertArgs a, int n_tiles) {
     using T = __bf16;
     using L = DirectTile<BM, BN, WM, WN, T>;
-    constexpr int NT = L::NT;
-    __shared__ __attribute__((aligned(1024))) char lds[L::LDS];
+    using F = Elt<T>::Frag;
+    constexpr int NT = L::NT, NM = WM / 32, NN = WN / 32;
+    __shared__ __attribute__((aligned(1024))) char m0[L::A_BYTES], m1[L::A_BYTES], w0[L::B_BYTES], w1[L::B_BYTES];
+    __shared__ __attribute__((aligned(1024))) char epi[L::EPI];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave % (BM / WM), wn = wave / (BM / WM);
-    const TileAt at = tile_at(blockIdx.x, gridDim.x, v_tiles, n_tiles);
-    if (at.v < 0 || at.nt >= n_tiles) return;
-    const Group g = find_group(a, at.v, BM, a.n_experts + 1);
-    const int rows = (int)(g.hi - g.lo);
-    if (rows <= 0) return;
-    const int64_t n0 = (int64_t)at.nt * BN;
     const int64_t K = GRAD ? a.d_out : a.d_in, N = GRAD ? a.d_in : a.d_out;
-    T* const y = (T*)a.y + g.lo * a.ld_y;
-    if (g.e == a.n_experts) {
-        zero_rows<T, BN, NT>(y, a.ld_y, rows, n0, N, tid);
-        return;
-    }
-    const T* const w = (const T*)a.w + (int64_t)g.e * a.d_in * a.d_out;
     const uint32_t width = (uint32_t)(K * 2);
-    const int n_left = (int)(N - n0 < BN ? N - n0 : BN);
-
     const bool through = !GRAD && a.order;
     const int64_t lda = GRAD ? a.ld_dz : a.ld_x;
-    const T* const abase = GRAD ? (const T*)a.dz + g.lo * lda : through ? (const T*)a.x : (const T*)a.x + g.lo * lda;
-    const __amdgpu_buffer_rsrc_t ra =
-        rsrc_of(uniform(abase), uniform((int)(uint32_t)(((through ? a.x_rows : rows) - 1) * lda * 2 + K * 2)));
-    CopyRows<BM, NT> ca;
-    ca.init(
-        [&](int r) -> uint32_t {
-            if (r >= rows) return kBufferOutOfRange;
-            if (!through) return (uint32_t)(r * lda * 2);
-            const int64_t t = x_row(a, g.lo + r);
-            return t < 0 ? kBufferOutOfRange : (uint32_t)(t * lda * 2);
-        },
-        wave, lane);
-    // forward: rows of W; gradient: its columns
-    CopyRows<BN, NT> cb;
-    CopyCols<BN, NT> cc;
-    const __amdgpu_buffer_rsrc_t rb = rsrc_of(uniform(w + n0 * K), uniform((int)(n_left * K * 2)));
-    const ColsSource wc{uniform(w + n0), (int)(N * 2), (int)(n0 * 2), (int)K};
-    if (GRAD)
-        cc.init((uint32_t)(N * 2), n_left, wave, lane);
-    else
-        cb.init([&](int r) { return r < n_left ? (uint32_t)(r * K * 2) : kBufferOutOfRange; }, wave, lane);
 
-    f32x16 acc[WM / 32][WN / 32];
-    rows_start<GRAD, WM, WN>(a, g.e, acc, n0 + wn * WN, N, lane);
-    auto stage_at = [&](int st) { return lds + st * L::STAGE; };
-    __amdgpu_buffer_rsrc_t rk = rb;
-    product_loop<WM / 32, WN / 32, L::QA + L::QB>(
-        acc, (int)((K + 63) / 64),
-        [&](int st, int j, int q) { return frag_rows<T>(stage_at(st), wm * WM + 32 * j, q, lane); },
-        [&](int st, int i, int q) {
-            const char* tb = stage_at(st) + L::A_BYTES;
-            return GRAD ? frag_cols<T, BN>(tb, wn * WN + 32 * i, q, lane)
-                        : frag_rows<T>(tb, wn * WN + 32 * i, q, lane);
-        },
-        [&](int c, int t) {
-            char* slot = stage_at(t & 1);
-            if (c < L::QA)
-                ca.issue(c, ra, slot, (uint32_t)t * kStepBytes, width, wave);
-            else if constexpr (!GRAD)
-                cb.issue(c - L::QA, rb, slot + L::A_BYTES, (uint32_t)t * kStepBytes, width, wave);
-            else
-                cc.issue(c - L::QA, rk, slot + L::A_BYTES, wave);
-        },
-        [&](int t) {
-            if (GRAD) rk = wc.step(t);
-        },
-        [](const Elt<T>::Frag (&)[WM / 32]) {});
-    rows_epilogue<T, GRAD, WM, WN, true>(a, g, lds + wave * epilogue_bytes<T, WN>(), acc, y, rows, wm * WM,
-                                         n0 + wn * WN, N, lane);
+    TileWalk<BM> walk;
+    walk.start(a, n_tiles);
+    struct Tile {
+        Group g;
+        int64_t n0;
+        int rows, n_left;
+    } cur, nxt;
+    int pair[L::QA];  // through the order: the next tile's slots, loaded a tile ahead
+    // the next tile with an expert; slots without one become zero rows on the way
+    auto advance = [&](Tile& t) {
+        int nt = 0;
+        while (walk.next(a, t.g, nt)) {
+            t.n0 = (int64_t)nt * BN;
+            t.rows = uniform(t.g.hi - t.g.lo);
+            t.n_left = (int)(N - t.n0 < BN ? N - t.n0 : BN);
+            if (t.g.e < a.n_experts) {
+                if (through)
+#pragma unroll
+                    for (int q = 0; q < L::QA; ++q) {
+                        const int r = CopyRows<BM, NT>::row(q, wave, again(lane));
+                        pair[q] = r < t.rows ? a.order[t.g.lo + r] : -1;
+                    }
+                return;
+            }
+            zero_rows<T, BN, NT>((T*)a.y + (int64_t)t.g.lo * a.ld_y, a.ld_y, t.rows, t.n0, N, tid);
+        }
+        t.rows = 0;
+    };
+
+    // sources of the tile that is being copied (none left: nothing in range)
+    __amdgpu_buffer_rsrc_t ra, rb;
+    CopyRows<BM, NT> ca;
+    CopyRows<BN, NT> cb;  // forward: rows of W
+    CopyCols<BN, NT> cc;  // gradient: its columns
+    ColsSource wc;
+    auto source = [&](const Tile& t) {
+        const int ln = again(lane);
+        const T* const w = (const T*)a.w + (t.rows ? (int64_t)t.g.e * a.d_in * a.d_out : 0);
+        const int64_t lo = t.rows ? (int64_t)t.g.lo : 0;
+        const T* const base = GRAD ? (const T*)a.dz + lo * lda : through ? (const T*)a.x : (const T*)a.x + lo * lda;
+        const int64_t bytes = ((through ? a.x_rows : t.rows) - 1) * lda * 2 + K * 2;
+        ra = rsrc_of(uniform(base), uniform(t.rows ? (int)(uint32_t)bytes : 0));
+        ca.init(
+            [&](int q, int r) -> uint32_t {
+                if (r >= t.rows) return kBufferOutOfRange;
+                if (!through) return (uint32_t)(r * lda * 2);
+                const int64_t row = row_of_pair(a, pair[q]);
+                return row < 0 ? kBufferOutOfRange : (uint32_t)(row * lda * 2);
+            },
+            width, wave, ln);
+        const int cols = t.rows ? t.n_left : 0;
+        if (GRAD) {
+            wc = ColsSource{uniform(w + t.n0), (int)(N * 2), (int)(t.n0 * 2), cols ? (int)K : 0};
+            cc.init((uint32_t)(N * 2), cols, wave, ln);
+        } else {
+            rb = rsrc_of(uniform(w + t.n0 * K), uniform((int)(cols * K * 2)));
+            cb.init([&](int, int r) { return r < cols ? (uint32_t)(r * K * 2) : kBufferOutOfRange; }, width, wave, ln);
+        }
+    };
+    auto copy = [&](int c, char* ms, char* ws, int t) {
+        if (c < L::QA)
+            ca.issue(c, ra, ms, (uint32_t)t * kStepBytes, width, wave);
+        else if constexpr (!GRAD)
+            cb.issue(c - L::QA, rb, ws, (uint32_t)t * kStepBytes, width, wave);
+        else
+            cc.issue(c - L::QA, rb, ws, wave);
+    };
+    auto ready = [&](int t) {
+        if (GRAD) rb = wc.step(t);
+    };
+    auto read = [&](int r, const char* ms, const char* ws, int q, F(&fm)[NM], F(&fn)[NN]) {
+        if (r < NM)
+            fm[r] = frag_rows<T>(ms, wm * WM + 32 * r, q, lane);
+        else
+            fn[r - NM] = GRAD ? frag_cols<T, BN>(ws, wn * WN + 32 * (r - NM), q, lane)
+                              : frag_rows<T>(ws, wn * WN + 32 * (r - NM), q, lane);
+    };
+
+    // steps, rounded up to whole rounds of both stages (a step past K is zeros)
+    const int nk = 2 * (int)((K + 127) / 128);
+    advance(cur);
+    if (cur.rows == 0) return;
+    source(cur);
+    ready(0);
+#pragma unroll
+    for (int c = 0; c < L::QA + L::QB; ++c) copy(c, m0, w0, 0);
+    wait_copies_barrier();
+    ready(1);
+#pragma unroll
+    for (int c = 0; c < L::QA + L::QB; ++c) copy(c, m1, w1, 1);
+    Frags<NM, NN> f;
+#pragma unroll
+    for (int r = 0; r < NM + NN; ++r) read(r, m0, w0, 0, f.m[0], f.n[0]);
+
+    // tile after tile without a pause: the last two steps of one copy the
+    // first two of the next, which is in flight while the one's rows are stored
+    while (true) {
+        advance(nxt);
+        f32x16 acc[NM][NN];
+        rows_start<GRAD, WM, WN>(a, cur.g.e, acc, cur.n0 + wn * WN, N, again(lane));
+        int done = 0;  // steps of the copied tile's predecessor
+        for (int t = 0; t < nk; t += 2) {
+            product_step<NM, NN, L::QA + L::QB>(
+                acc, f,
+                [&](int r, auto next, int q, F(&fm)[NM], F(&fn)[NN]) {
+                    if constexpr (decltype(next)::value)
+                    read(r, m1, w1, q, fm, fn);
+                else
+                    read(r, m0, w0, q, fm, fn);
+                },
+                [&]() {
+                    if (t + 2 == nk) {
+                        source(nxt);
+                        done = nk;
+                    }
+                    ready(t + 2 - done);
+                },
+                [&](int c) { copy(c, m0, w0, t + 2 - done); }, [](const F(&)[NM]) {});
+            product_step<NM, NN, L::QA + L::QB>(
+                acc, f,
+                [&](int r, auto next, int q, F(&fm)[NM], F(&fn)[NN]) {
+                    if constexpr (decltype(next)::value)
+                    read(r, m0, w0, q, fm, fn);
+                else
+                    read(r, m1, w1, q, fm, fn);
+                },
+                [&]() { ready(t + 3 - done); }, [&](int c) { copy(c, m1, w1, t + 3 - done); }, [](const F(&)[NM]) {});
+        }
+        rows_epilogue<T, GRAD, WM, WN, true>(a, cur.g, epi + wave * epilogue_bytes<T, WN>(), acc,
+                                             (T*)a.y + (int64_t)cur.g.lo * a.ld_y, cur.rows, wm * WM, cur.n0 + wn * WN, N,
+                                             again(lane));
+        if (nxt.rows == 0) break;
+        cur = nxt;
+    }
+    wait_copies_barrier();  // (no copy outlives its workgroup)
 }
 
 // ---------------------------------------------------------------------------
@@ -696,9 +824,24 @@ struct WeightWork {
 };
 __device__ __forceinline__ WeightWork weight_work(const ExpertArgs& a, int64_t b, int m_tiles, int n_tiles, int BM,
                                                   int BN) {
+    // Workgroup b runs on XCD b % 8.  Each XCD gets an eighth of every item's
+    // tiles, neighbouring ones (they read the same columns of dz, and few of
+    // x), and the items in the same order; which eighth rotates.
     WeightWork w;
-    const int tile = (int)(b % (m_tiles * n_tiles));
-    const int64_t v = b / (m_tiles * n_tiles), M = a.d_out, N = a.d_in;
+    w.any = false;
+    const int tiles = m_tiles * n_tiles, most = (tiles + 7) / 8;
+    const int64_t M = a.d_out, N = a.d_in;
+    int64_t v;
+    int tile;
+    if (tiles < 8) {  // (fewer tiles than XCDs: nothing to share)
+        v = b / tiles;
+        tile = (int)(b % tiles);
+    } else {
+        v = (b >> 3) / most;
+        const int part = (int)((b + v) & 7);
+        tile = part * tiles / 8 + (int)((b >> 3) % most);
+        if (tile >= (part + 1) * tiles / 8) return w;
+    }
     w.m0 = (int64_t)(tile / n_tiles) * BM;
     w.n0 = (int64_t)(tile % n_tiles) * BN;
     if (a.chunk) {
@@ -728,7 +871,7 @@ __device__ __forceinline__ void weights_epilogue(const ExpertArgs& a, const Weig
             if (lane < 32 && mw + 32 * j + lane < M) w.bout[mw + 32 * j + lane] = b;
         }
         epilogue_block<float, WN>(
-            st, acc[j], lane, [](float x, int) { return x; },
+            st, acc[j], lane, [](float x) { return x; },
             [&](int m, int n, typename RowIO<float>::Vec x) {
                 const int64_t r = mw + 32 * j + m;
                 if (r < M && nw + n < N) RowIO<float>::store(w.out + r * N, nw + n, N, x);
@@ -829,14 +972,17 @@ __global__ void __launch_bounds__((DirectTile<BM, BN, WM, WN, float>::NT))
     using L = DirectTile<BM, BN, WM, WN, float>;
     constexpr int NT = L::NT;
     using CB = CopyCols<BN, NT>;
-    __shared__ __attribute__((aligned(1024))) char lds[L::LDS];
+    using F = Elt<T>::Frag;
+    constexpr int NM = WM / 32, NN = WN / 32;
+    static_assert(L::EPI <= 2 * L::A_BYTES, "rows leave through the first operand's stages");
+    __shared__ __attribute__((aligned(1024))) char m0[L::A_BYTES], m1[L::A_BYTES], w0[L::B_BYTES], w1[L::B_BYTES];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave % (BM / WM), wn = wave / (BM / WM);
     const WeightWork w = weight_work(a, blockIdx.x, m_tiles, n_tiles, BM, BN);
     if (!w.any) return;
     const Group g = w.g;
     const bool with_bias = w.bout && wn == 0;
-    const int rows = uniform((int)(g.hi > g.lo ? g.hi - g.lo : 0));
+    const int rows = uniform(g.hi > g.lo ? g.hi - g.lo : 0);
     const int m_left = (int)(a.d_out - w.m0 < BM ? a.d_out - w.m0 : BM);
     const int n_left = (int)(a.d_in - w.n0 < BN ? a.d_in - w.n0 : BN);
 
@@ -853,36 +999,82 @@ __global__ void __launch_bounds__((DirectTile<BM, BN, WM, WN, float>::NT))
     ca.init((uint32_t)zs.pitch, m_left, wave, lane);
     cb.init((uint32_t)xs.pitch, n_left, wave, lane);
     __amdgpu_buffer_rsrc_t rz = all, rx = all;
-    auto stage_at = [&](int st) { return lds + st * L::STAGE; };
-    product_loop<WM / 32, WN / 32, L::QA + L::QB>(
-        acc, (rows + 63) / 64,
-        [&](int st, int j, int q) { return frag_cols<T, BM>(stage_at(st), wm * WM + 32 * j, q, lane); },
-        [&](int st, int i, int q) { return frag_cols<T, BN>(stage_at(st) + L::A_BYTES, wn * WN + 32 * i, q, lane); },
-        [&](int c, int t) {
-            char* slot = stage_at(t & 1);
-            if (c < L::QA)
-                ca.issue(c, rz, slot, wave);
-            else
-                cb.issue(c - L::QA, rx, slot + L::A_BYTES, wave);
-        },
-        [&](int t) {
-            rz = zs.step(t);
-            if constexpr (THROUGH) {
+    int pair[CB::Q];  // through the order: the next copies' slots, loaded a step ahead
+    auto before = [&](int t) {
+        if constexpr (THROUGH)
 #pragma unroll
-                for (int q = 0; q < CB::Q; ++q) {
-                    const int64_t s = g.lo + 64 * (int64_t)t + CB::k_of(q, wave, lane);
-                    const int64_t r = s < g.hi ? x_row(a, s) : -1;
-                    const int c = CB::piece(q, wave, lane);
-                    cb.off[q] = r >= 0 && 8 * c < n_left ? (uint32_t)(r * a.ld_x * 2) + 16 * c : kBufferOutOfRange;
-                }
-            } else {
-                rx = xs.step(t);
+            for (int q = 0; q < CB::Q; ++q) {
+                const int s = 64 * t + CB::k_of(q, wave, lane);
+                pair[q] = s < rows ? a.order[g.lo + s] : -1;
             }
-        },
-        [&](const Elt<T>::Frag (&fm)[WM / 32]) {
-            if (with_bias) add_bias<T>(bsum, fm);
-        });
-    weights_epilogue<WM, WN>(a, w, lds + wave * epilogue_bytes<float, WN>(), acc, bsum, w.m0 + wm * WM,
+    };
+    auto ready = [&](int t) {
+        rz = zs.step(t);
+        if constexpr (THROUGH) {
+#pragma unroll
+            for (int q = 0; q < CB::Q; ++q) {
+                const int64_t r = row_of_pair(a, pair[q]);
+                const int c = CB::piece(q, wave, lane);
+                cb.off[q] = r >= 0 && 8 * c < n_left ? (uint32_t)(r * a.ld_x * 2) + 16 * c : kBufferOutOfRange;
+            }
+        } else {
+            rx = xs.step(t);
+        }
+    };
+    auto copy = [&](int c, char* ms, char* ws) {
+        if (c < L::QA)
+            ca.issue(c, rz, ms, wave);
+        else
+            cb.issue(c - L::QA, rx, ws, wave);
+    };
+    auto read = [&](int r, const char* ms, const char* ws, int q, F(&fm)[NM], F(&fn)[NN]) {
+        if (r < NM)
+            fm[r] = frag_cols<T, BM>(ms, wm * WM + 32 * r, q, lane);
+        else
+            fn[r - NM] = frag_cols<T, BN>(ws, wn * WN + 32 * (r - NM), q, lane);
+    };
+    auto bias = [&](const F(&fm)[NM]) {
+        if (with_bias) add_bias<T>(bsum, fm);
+    };
+    Frags<NM, NN> f;
+    if (rows) {
+        before(0);
+        ready(0);
+#pragma unroll
+        for (int c = 0; c < L::QA + L::QB; ++c) copy(c, m0, w0);
+        before(1);
+        wait_copies_barrier();
+        ready(1);
+#pragma unroll
+        for (int c = 0; c < L::QA + L::QB; ++c) copy(c, m1, w1);
+#pragma unroll
+        for (int r = 0; r < NM + NN; ++r) read(r, m0, w0, 0, f.m[0], f.n[0]);
+    }
+    // (steps past the last slot copy zeros)
+    for (int t = 0; 64 * t < rows; t += 2) {
+        before(t + 2);
+        product_step<NM, NN, L::QA + L::QB>(
+            acc, f,
+            [&](int r, auto next, int q, F(&fm)[NM], F(&fn)[NN]) {
+                if constexpr (decltype(next)::value)
+                    read(r, m1, w1, q, fm, fn);
+                else
+                    read(r, m0, w0, q, fm, fn);
+            },
+            [&]() { ready(t + 2); }, [&](int c) { copy(c, m0, w0); }, bias);
+        before(t + 3);
+        product_step<NM, NN, L::QA + L::QB>(
+            acc, f,
+            [&](int r, auto next, int q, F(&fm)[NM], F(&fn)[NN]) {
+                if constexpr (decltype(next)::value)
+                    read(r, m0, w0, q, fm, fn);
+                else
+                    read(r, m1, w1, q, fm, fn);
+            },
+            [&]() { ready(t + 3); }, [&](int c) { copy(c, m1, w1); }, bias);
+    }
+    wait_copies_barrier();
+    weights_epilogue<WM, WN>(a, w, (wave < NT / 128 ? m0 : m1) + wave % (NT / 128) * epilogue_bytes<float, WN>(), acc, bsum, w.m0 + wm * WM,
                              w.n0 + wn * WN, with_bias, lane);
 }
 
@@ -919,10 +1111,10 @@ template <bool GRAD, int BM, int BN, int WM, int WN>
 void run_rows_direct(const ExpertArgs& a, hipStream_t s) {
     const int64_t N = GRAD ? a.d_in : a.d_out;
     const int n_tiles = (int)((N + BN - 1) / BN);
-    const int64_t v_tiles = a.slots / BM + a.n_experts + 1;
-    const int64_t blocks = (v_tiles * n_tiles + 7) / 8 * 8;
+    const int64_t tiles = (a.slots / BM + a.n_experts + 1) * n_tiles;
+    const unsigned blocks = (unsigned)(tiles < kCus ? (tiles + 7) / 8 * 8 : kCus);
     k_expert_rows_direct<GRAD, BM, BN, WM, WN>
-        <<<(unsigned)blocks, DirectTile<BM, BN, WM, WN, __bf16>::NT, 0, s>>>(a, v_tiles, n_tiles);
+        <<<blocks, DirectTile<BM, BN, WM, WN, __bf16>::NT, 0, s>>>(a, n_tiles);
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -948,12 +1140,15 @@ void pick_rows(const ExpertArgs& a, hipStream_t s) {
         run_rows<T, GRAD, 128, 128, 64, 64>(a, s);
 }
 
+// Workgroups of `items` weight gradients of `tiles` tiles (as weight_work deals them out).
+int64_t weight_blocks(int64_t items, int tiles) { return tiles < 8 ? items * tiles : 8 * items * ((tiles + 7) / 8); }
+
 template <class T, int BM, int BN, int WM, int WN>
 void run_weights(const ExpertArgs& a, hipStream_t s) {
     const int mt = (a.d_out + BM - 1) / BM, nt = (a.d_in + BN - 1) / BN;
     const int64_t items = a.chunk ? a.slots / a.chunk + a.n_experts : a.n_experts;
     k_expert_weights<T, BM, BN, WM, WN>
-        <<<(unsigned)(items * mt * nt), WeightTile<T, BM, BN, WM, WN>::NT, 0, s>>>(a, mt, nt);
+        <<<(unsigned)weight_blocks(items, mt * nt), WeightTile<T, BM, BN, WM, WN>::NT, 0, s>>>(a, mt, nt);
 }
 
 template <int BM, int BN, int WM, int WN>
@@ -961,10 +1156,11 @@ void run_weights_direct(const ExpertArgs& a, hipStream_t s) {
     const int mt = (a.d_out + BM - 1) / BM, nt = (a.d_in + BN - 1) / BN;
     const int64_t items = a.chunk ? a.slots / a.chunk + a.n_experts : a.n_experts;
     constexpr int NT = DirectTile<BM, BN, WM, WN, float>::NT;
+    const unsigned blocks = (unsigned)weight_blocks(items, mt * nt);
     if (a.order)
-        k_expert_weights_direct<true, BM, BN, WM, WN><<<(unsigned)(items * mt * nt), NT, 0, s>>>(a, mt, nt);
+        k_expert_weights_direct<true, BM, BN, WM, WN><<<blocks, NT, 0, s>>>(a, mt, nt);
     else
-        k_expert_weights_direct<false, BM, BN, WM, WN><<<(unsigned)(items * mt * nt), NT, 0, s>>>(a, mt, nt);
+        k_expert_weights_direct<false, BM, BN, WM, WN><<<blocks, NT, 0, s>>>(a, mt, nt);
 }
 
 // Whether the weight kernels may copy directly.
