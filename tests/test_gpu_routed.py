@@ -142,7 +142,8 @@ def test_rows_there_and_back(n, k, E, d, drop, bf16, pad):
 LAYERS = [(1, 1, 1, 1, 1, 0.0), (1, 2, 16, 64, 96, 0.0), (1, 2, 16, 1024, 512, 0.0), (5, 3, 4, 63, 32, 0.3),
           (100, 1, 60, 63, 32, 0.4), (300, 2, 3, 64, 64, 0.0), (300, 2, 3, 256, 256, 0.2), (257, 1, 1, 319, 255, 0.0),
           (500, 2, 5, 130, 33, 0.1), (64, 1, 4, 8, 8, 1.0), (700, 3, 2, 40, 520, 0.1), (130, 1, 64, 16, 16, 0.0),
-          (1500, 2, 4, 128, 192, 0.1), (2500, 2, 3, 72, 96, 0.05), (2100, 1, 100, 32, 24, 0.0), (900, 2, 2, 264, 384, 0.0)]
+          (1500, 2, 4, 128, 192, 0.1), (2500, 2, 3, 72, 96, 0.05), (2100, 1, 100, 32, 24, 0.0), (900, 2, 2, 264, 384, 0.0),
+          (25000, 2, 3, 264, 264, 0.05), (20000, 2, 5, 264, 272, 0.0), (3000, 3, 70, 104, 128, 0.1)]
 
 
 @pytest.mark.parametrize("through_order", [False, True])

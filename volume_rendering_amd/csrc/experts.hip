@@ -17,14 +17,27 @@ namespace nerf {
 
 namespace {
 
-#ifndef NERF_RT
-#define NERF_RT 256, 256, 128, 64
-#endif
-#ifndef NERF_WT
-#define NERF_WT 256, 256, 128, 64
-#endif
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
+constexpr int64_t kDirectBytes = ((int64_t)1 << 32) - 65536;  // extent one buffer resource may cover
+
+// The same value, which the compiler takes for a new one: what depends on it is
+// computed where it is used, once a tile, and not kept in registers across the
+// loop over k.
+__device__ __forceinline__ int again(int v) {
+    asm volatile("" : "+v"(v));
+    return v;
+}
+// Values that are the same in every lane, kept in scalar registers.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ uint64_t uniform(const void* p) {
+    const uint64_t v = reinterpret_cast<uint64_t>(p);
+    return (uint64_t)(uint32_t)uniform((int)(v >> 32)) << 32 | (uint32_t)uniform((int)v);
+}
+// base and bytes uniform; bytes as an unsigned number
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_of(uint64_t base, int bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(base), (short)0, bytes, kBufferWord3);
+}
 // ---------------------------------------------------------------------------
 // Which expert a workgroup works for.  Experts' row counts are known on the
 // device only, so workgroups are numbered by "virtual tiles": expert e starts
@@ -288,29 +301,40 @@ __device__ __forceinline__ void rows_start(const ExpertArgs& a, int e, f32x16 (&
 }
 
 // A wave's WM x WN block of y (ReLU) or dx (the mask of x), from row r0 of the
-// group's `rows` and column nw.  WHOLE: N is a multiple of a piece.
-template <class T, bool GRAD, int WM, int WN, bool WHOLE = false>
+// group's `rows` and column nw.  DIRECT: 16-byte aligned rows of whole pieces,
+// stored through a buffer resource, lanes outside the tile out of its range:
+// every wave then issues exactly WM / 32 * WN / 16 stores, which the product
+// loop counts.
+template <class T, bool GRAD, int WM, int WN, bool DIRECT = false>
 __device__ __forceinline__ void rows_epilogue(const ExpertArgs& a, const Group& g, char* st,
                                               const f32x16 (&acc)[WM / 32][WN / 32], T* y, int rows, int r0,
                                               int64_t nw, int64_t N, int lane) {
     const float floor = !GRAD && a.relu ? 0.0f : -INFINITY;
+    const __amdgpu_buffer_rsrc_t ry =
+        rsrc_of(uniform(y), uniform((int)(uint32_t)((rows - 1) * a.ld_y * (int)sizeof(T) + N * (int)sizeof(T))));
 #pragma unroll
     for (int j = 0; j < WM / 32; ++j) {
         epilogue_block<T, WN>(
             st, acc[j], lane, [&](float v) { return v < floor ? floor : v; },  // (a NaN stays)
             [&](int m, int n, typename RowIO<T>::Vec v) {
                 const int r = r0 + 32 * j + m;
-                if (r >= rows || nw + n >= N) return;
+                const bool in = r < rows && nw + n < N;
+                if constexpr (!DIRECT)
+                    if (!in) return;
                 if (GRAD && a.relu) {
-                    const int64_t t = x_row(a, g.lo + r);
+                    const int64_t t = in ? x_row(a, g.lo + r) : -1;
                     const typename RowIO<T>::Vec x =
                         t < 0 ? RowIO<T>::zero()
-                              : RowIO<T>::load((const T*)a.x + t * a.ld_x, nw + n, WHOLE ? INT64_MAX : N);
+                              : RowIO<T>::load((const T*)a.x + t * a.ld_x, nw + n, DIRECT ? INT64_MAX : N);
 #pragma unroll
                     for (int e = 0; e < RowIO<T>::PER; ++e)
                         if (!(RowIO<T>::get(x, e) > 0.0f)) v.e[e] = (T)0.0f;
                 }
-                RowIO<T>::store(y + (int64_t)r * a.ld_y, nw + n, WHOLE ? INT64_MAX : N, v);
+                if constexpr (DIRECT)
+                    __builtin_amdgcn_raw_buffer_store_b128(
+                        v.u, ry, in ? (uint32_t)((r * a.ld_y + nw + n) * (int)sizeof(T)) : kBufferOutOfRange, 0, 0);
+                else
+                    RowIO<T>::store(y + (int64_t)r * a.ld_y, nw + n, N, v);
             });
     }
 }
@@ -414,65 +438,38 @@ __global__ void __launch_bounds__((RowsTile<T, GRAD, BM, BN, WM, WN>::NT))
 // Pieces past the matrix get an offset out of the buffer's range, which copies
 // zeros.
 // ---------------------------------------------------------------------------
-constexpr int64_t kDirectBytes = ((int64_t)1 << 32) - 65536;  // extent one buffer resource may cover
-
-// The same value, which the compiler takes for a new one: what depends on it is
-// computed where it is used, once a tile, and not kept in registers across the
-// loop over k.
-__device__ __forceinline__ int again(int v) {
-    asm volatile("" : "+v"(v));
-    return v;
-}
-// Values that are the same in every lane, kept in scalar registers.
-__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
-__device__ __forceinline__ uint64_t uniform(const void* p) {
-    const uint64_t v = reinterpret_cast<uint64_t>(p);
-    return (uint64_t)(uint32_t)uniform((int)(v >> 32)) << 32 | (uint32_t)uniform((int)v);
-}
-// base and bytes uniform; bytes as an unsigned number
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_of(uint64_t base, int bytes) {
-    return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(base), (short)0, bytes, kBufferWord3);
-}
 __device__ __forceinline__ void copy16(__amdgpu_buffer_rsrc_t r, char* dst, uint32_t off) {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (void NERF_LDS_PTR)dst, 16, (int)off, 0, 0, 0);
 }
-// This wave's copies have arrived and its LDS reads are done; then all waves'.
-// (__syncthreads() would do the same with a wait for stores in flight.)
+// All but the wave's N latest copies have arrived, and its LDS reads are done;
+// then all waves'.
+template <int N>
 __device__ __forceinline__ void wait_copies_barrier() {
     asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt(7 << 4);  // vmcnt(0) lgkmcnt(0)
+    __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | ((N >> 4) << 14));  // vmcnt(N) lgkmcnt(0)
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
 }
 
 template <int R, int NT>
 struct CopyRows {  // R rows, k contiguous
-    static constexpr int Q = R * 8 / NT;
+    static constexpr int NW = NT / 64, Q = R * 8 / NT, APART = 8 * NW;  // rows between a wave's copies
     static_assert(R * 8 % NT == 0, "whole copies");
-    uint32_t off[Q];
-    static __device__ __forceinline__ int row(int q, int wave, int lane) { return (wave * Q + q) * 8 + (lane >> 3); }
+    static __device__ __forceinline__ int row(int q, int wave, int lane) {
+        return (q * NW + wave) * 8 + (lane >> 3);
+    }
     // byte of a lane's piece within a k-step
     static __device__ __forceinline__ uint32_t piece(int q, int wave, int lane) {
         return (uint32_t)((lane & 7) ^ swz_row(row(q, wave, lane))) << 4;
     }
-    uint32_t part;  // bit q: copy q's piece is inside the last, partial step
-    // row_off(q, r): byte offset of row r of `width` bytes, or kBufferOutOfRange
-    template <class F>
-    __device__ __forceinline__ void init(F&& row_off, uint32_t width, int wave, int lane) {
-        part = 0;
-#pragma unroll
-        for (int q = 0; q < Q; ++q) {
-            const uint32_t o = row_off(q, row(q, wave, lane)), pc = piece(q, wave, lane);
-            off[q] = o == kBufferOutOfRange ? o : o + pc;
-            part |= (pc < width % kStepBytes ? 1u : 0u) << q;
-        }
-    }
-    // copy q of the k-step at byte kb
-    __device__ __forceinline__ void issue(int q, __amdgpu_buffer_rsrc_t rs, char* tile, uint32_t kb, uint32_t width,
-                                          int wave) const {
-        uint32_t o = __builtin_elementwise_add_sat(off[q], kb);  // (out of range stays so)
-        if (kb + kStepBytes > width) o = kb < width && (part >> q & 1) ? o : kBufferOutOfRange;
-        copy16(rs, tile + (wave * Q + q) * 1024, o);
+    // copy q, whose row starts at byte `off` (its lane's piece included), of
+    // the k-step at byte kb of rows of `width` bytes; `inside`: the piece is
+    // inside a last, partial step
+    static __device__ __forceinline__ void issue(int q, __amdgpu_buffer_rsrc_t rs, char* tile, uint32_t off,
+                                                 uint32_t kb, uint32_t width, bool inside, int wave) {
+        uint32_t o = __builtin_elementwise_add_sat(off, kb);  // (out of range stays so)
+        if (kb + kStepBytes > width) o = kb < width && inside ? o : kBufferOutOfRange;
+        copy16(rs, tile + (q * NW + wave) * 1024, o);
     }
 };
 
@@ -499,8 +496,8 @@ struct CopyCols {  // one k-step (64 rows) of a k-major matrix, C columns
     }
 };
 
-// k-steps of a k-major matrix: `rows` rows `pitch` bytes apart from base on,
-// which is `c0` bytes into the first.
+// k-steps of 64 rows of a k-major matrix: `rows` rows `pitch` bytes apart from
+// base on, which is `c0` bytes into the first.
 struct ColsSource {
     uint64_t base;
     int pitch, c0, rows;
@@ -516,15 +513,19 @@ struct ColsSource {
 // ---------------------------------------------------------------------------
 // One k-step of 64 of a product, in two LDS stages (an array for each stage of
 // each operand: the compiler then sees that reads need not wait for copies in
-// flight, which go into other arrays).
-// Fragments of the next 16 k are read while the current ones multiply, a read
-// or a copy between each two matrix instructions.  In a step's last quarter
-// every wave has its fragments in registers, so after one barrier the stage is
-// free: the copies of the step after next start there, and have a step's
-// multiplications to arrive in.
-//   read(r, next, q, fm, fn): part r of NM + NN of the fragments of quarter q
+// flight, which go into other arrays).  The fragments of the next 16 k are read
+// while the current ones multiply, a read or a copy between each two matrix
+// instructions.  In a step's last quarter every wave has its fragments in
+// registers, so after one barrier the stage is free: the copies of the step
+// after next start there and have a step's multiplications to arrive in.  (Four
+// stages of 32 k, three of them in flight, took the same time.)
+//   stores: at that barrier the STORES rows stored since the awaited copies may
+//   still be in flight;
+//   read(r, next, q, fm, fn): piece r of NM + NN of the fragments of quarter q
 //   of this step or (next) of quarter 0 of the next one;
-//   ready(): a step's copies are about to start;  copy(c): copy c of them;
+//   ready(): a step's copies are about to start (called before the barrier with
+//   EARLY: its work then overlaps the wait, but holds registers across it);
+//   copy(c): copy c of them;
 //   extra(fm): further use of a quarter's fragments.
 // ---------------------------------------------------------------------------
 template <int NM, int NN>
@@ -532,25 +533,33 @@ struct Frags {
     Elt<__bf16>::Frag m[2][NM], n[2][NN];
 };
 
-template <int NM, int NN, int COPIES, class RD, class RY, class CP, class EX>
-__device__ __forceinline__ void product_step(f32x16 (&acc)[NM][NN], Frags<NM, NN>& f, RD&& read, RY&& ready, CP&& copy,
-                                             EX&& extra) {
+template <int COPIES, int STORES, bool EARLY, int NM, int NN, class RD, class RY, class CP, class EX>
+__device__ __forceinline__ void product_step(f32x16 (&acc)[NM][NN], Frags<NM, NN>& f, bool stores, RD&& read,
+                                             RY&& ready, CP&& copy, EX&& extra) {
     constexpr int CPM = (COPIES + NM * NN - 1) / (NM * NN), RPM = (NM + NN + NM * NN - 1) / (NM * NN);
-    auto quarter = [&](auto qc) {
+    auto part = [&](auto qc) {
         constexpr int q = decltype(qc)::value;
-        if constexpr (q == 3) {
-            wait_copies_barrier();
+        constexpr bool last = q == 3;
+        if constexpr (last) {
+            if constexpr (EARLY) {
+                ready();
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            if (STORES > 0 && stores)
+                wait_copies_barrier<STORES>();
+            else
+                wait_copies_barrier<0>();
             __builtin_amdgcn_sched_barrier(0);
-            ready();
+            if constexpr (!EARLY) ready();
         }
 #pragma unroll
         for (int m = 0; m < NM * NN; ++m) {
 #pragma unroll
             for (int u = 0; u < RPM; ++u)
                 if (m * RPM + u < NM + NN)
-                    read(m * RPM + u, std::integral_constant<bool, q == 3>{}, (q + 1) & 3, f.m[(q + 1) & 1],
+                    read(m * RPM + u, std::integral_constant<bool, last>{}, last ? 0 : q + 1, f.m[(q + 1) & 1],
                          f.n[(q + 1) & 1]);
-            if constexpr (q == 3)
+            if constexpr (last)
 #pragma unroll
                 for (int u = 0; u < CPM; ++u)
                     if (m * CPM + u < COPIES) copy(m * CPM + u);
@@ -559,10 +568,10 @@ __device__ __forceinline__ void product_step(f32x16 (&acc)[NM][NN], Frags<NM, NN
         }
         extra(f.m[q & 1]);
     };
-    quarter(std::integral_constant<int, 0>{});
-    quarter(std::integral_constant<int, 1>{});
-    quarter(std::integral_constant<int, 2>{});
-    quarter(std::integral_constant<int, 3>{});
+    part(std::integral_constant<int, 0>{});
+    part(std::integral_constant<int, 1>{});
+    part(std::integral_constant<int, 2>{});
+    part(std::integral_constant<int, 3>{});
 }
 
 template <int BM, int BN, int WM, int WN, class O>
@@ -571,6 +580,7 @@ struct DirectTile {
     static constexpr int A_BYTES = BM * kStepBytes, B_BYTES = BN * kStepBytes;  // a stage of each operand
     static constexpr int EPI = (NT / 64) * epilogue_bytes<O, WN>();
     static constexpr int QA = BM * 8 / NT, QB = BN * 8 / NT;  // copies of each operand per wave and step
+    static constexpr int COPIES = QA + QB;
 };
 
 // ---------------------------------------------------------------------------
@@ -584,12 +594,13 @@ struct DirectTile {
 constexpr int kCus = 256;  // workgroups of a grid that stays: one per CU
 constexpr int kGroupTiles = 4;
 
-template <int BM>
 struct TileWalk {
+    int BM;  // slots per tile
     int l, end, v_tiles, step, n_tiles;
     int off, upto;  // lane e: first slot of expert e; tiles of experts 0 .. e
 
-    __device__ __forceinline__ void start(const ExpertArgs& a, int n) {
+    __device__ __forceinline__ void start(const ExpertArgs& a, int height, int n) {
+        BM = height;
         n_tiles = n;
         const int groups = a.n_experts + 1;
         if (groups <= 64) {
@@ -636,7 +647,7 @@ struct TileWalk {
 
 template <bool GRAD, int BM, int BN, int WM, int WN>
 __global__ void __launch_bounds__((DirectTile<BM, BN, WM, WN, __bf16>::NT))
-    k_expert_rows_direct(ExpertArgs a, int n_tiles) {
+    k_expert_rows_direct(ExpertArgs a, int tile_rows, int n_tiles) {
     using T = __bf16;
     using L = DirectTile<BM, BN, WM, WN, T>;
     using F = Elt<T>::Frag;
@@ -650,8 +661,8 @@ __global__ void __launch_bounds__((DirectTile<BM, BN, WM, WN, __bf16>::NT))
     const bool through = !GRAD && a.order;
     const int64_t lda = GRAD ? a.ld_dz : a.ld_x;
 
-    TileWalk<BM> walk;
-    walk.start(a, n_tiles);
+    TileWalk walk;
+    walk.start(a, tile_rows, n_tiles);
     struct Tile {
         Group g;
         int64_t n0;
@@ -679,12 +690,19 @@ __global__ void __launch_bounds__((DirectTile<BM, BN, WM, WN, __bf16>::NT))
         t.rows = 0;
     };
 
-    // sources of the tile that is being copied (none left: nothing in range)
+    // sources of the tile that is being copied (none left: nothing in range);
+    // rows past the tile's are past the end of its resource
+    using CA = CopyRows<BM, NT>;
+    using CB = CopyRows<BN, NT>;
     __amdgpu_buffer_rsrc_t ra, rb;
-    CopyRows<BM, NT> ca;
-    CopyRows<BN, NT> cb;  // forward: rows of W
-    CopyCols<BN, NT> cc;  // gradient: its columns
+    uint32_t oa[L::QA], ob[2];    // forward: rows of W, the first two copies
+    CopyCols<BN, NT> cc;   // gradient: its columns
     ColsSource wc;
+    // (the swizzle of a wave's copies is the same in all of them, or alternates
+    // between two)
+    static_assert(CA::APART % 32 == 0, "one swizzle in every second copy");
+    const bool inside[2] = {CA::piece(0, wave, lane) < width % kStepBytes,
+                            CA::piece(1, wave, lane) < width % kStepBytes};
     auto source = [&](const Tile& t) {
         const int ln = again(lane);
         const T* const w = (const T*)a.w + (t.rows ? (int64_t)t.g.e * a.d_in * a.d_out : 0);
@@ -692,28 +710,29 @@ __global__ void __launch_bounds__((DirectTile<BM, BN, WM, WN, __bf16>::NT))
         const T* const base = GRAD ? (const T*)a.dz + lo * lda : through ? (const T*)a.x : (const T*)a.x + lo * lda;
         const int64_t bytes = ((through ? a.x_rows : t.rows) - 1) * lda * 2 + K * 2;
         ra = rsrc_of(uniform(base), uniform(t.rows ? (int)(uint32_t)bytes : 0));
-        ca.init(
-            [&](int q, int r) -> uint32_t {
-                if (r >= t.rows) return kBufferOutOfRange;
-                if (!through) return (uint32_t)(r * lda * 2);
-                const int64_t row = row_of_pair(a, pair[q]);
-                return row < 0 ? kBufferOutOfRange : (uint32_t)(row * lda * 2);
-            },
-            width, wave, ln);
+#pragma unroll
+        for (int q = 0; q < L::QA; ++q) {
+            const int64_t row = through ? row_of_pair(a, pair[q]) : CA::row(q, wave, ln);
+            oa[q] = row < 0 ? kBufferOutOfRange : (uint32_t)(row * lda * 2) + CA::piece(q, wave, ln);
+        }
         const int cols = t.rows ? t.n_left : 0;
         if (GRAD) {
             wc = ColsSource{uniform(w + t.n0), (int)(N * 2), (int)(t.n0 * 2), cols ? (int)K : 0};
             cc.init((uint32_t)(N * 2), cols, wave, ln);
         } else {
             rb = rsrc_of(uniform(w + t.n0 * K), uniform((int)(cols * K * 2)));
-            cb.init([&](int, int r) { return r < cols ? (uint32_t)(r * K * 2) : kBufferOutOfRange; }, width, wave, ln);
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+                ob[q] = (uint32_t)(CB::row(q, wave, ln) * K * 2) + CB::piece(q, wave, ln);
         }
     };
     auto copy = [&](int c, char* ms, char* ws, int t) {
+        const uint32_t kb = (uint32_t)t * kStepBytes;
+        const int q = c < L::QA ? c : c - L::QA;
         if (c < L::QA)
-            ca.issue(c, ra, ms, (uint32_t)t * kStepBytes, width, wave);
+            CA::issue(q, ra, ms, oa[q], kb, width, inside[q & 1], wave);
         else if constexpr (!GRAD)
-            cb.issue(c - L::QA, rb, ws, (uint32_t)t * kStepBytes, width, wave);
+            CB::issue(q, rb, ws, ob[q & 1] + (uint32_t)((q & ~1) * CB::APART * K * 2), kb, width, inside[q & 1], wave);
         else
             cc.issue(c - L::QA, rb, ws, wave);
     };
@@ -735,30 +754,35 @@ __global__ void __launch_bounds__((DirectTile<BM, BN, WM, WN, __bf16>::NT))
     source(cur);
     ready(0);
 #pragma unroll
-    for (int c = 0; c < L::QA + L::QB; ++c) copy(c, m0, w0, 0);
-    wait_copies_barrier();
+    for (int c = 0; c < L::COPIES; ++c) copy(c, m0, w0, 0);
     ready(1);
 #pragma unroll
-    for (int c = 0; c < L::QA + L::QB; ++c) copy(c, m1, w1, 1);
+    for (int c = 0; c < L::COPIES; ++c) copy(c, m1, w1, 1);
+    wait_copies_barrier<L::COPIES>();
     Frags<NM, NN> f;
 #pragma unroll
     for (int r = 0; r < NM + NN; ++r) read(r, m0, w0, 0, f.m[0], f.n[0]);
 
-    // tile after tile without a pause: the last two steps of one copy the
-    // first two of the next, which is in flight while the one's rows are stored
+    // tile after tile without a pause: the last two steps of one copy the first
+    // two of the next, which is in flight while the one's rows are stored
+    bool stored = false;
     while (true) {
         advance(nxt);
         f32x16 acc[NM][NN];
         rows_start<GRAD, WM, WN>(a, cur.g.e, acc, cur.n0 + wn * WN, N, again(lane));
         int done = 0;  // steps of the copied tile's predecessor
         for (int t = 0; t < nk; t += 2) {
-            product_step<NM, NN, L::QA + L::QB>(
-                acc, f,
+            // (a tile's first step waits for copies issued before the last
+            // tile's rows were stored)
+            int fresh = uniform(t == 0 && stored);
+            asm volatile("" : "+s"(fresh));  // (one loop, not one for each value)
+            product_step<L::COPIES, NM * WN / 16, GRAD>(
+                acc, f, fresh != 0,
                 [&](int r, auto next, int q, F(&fm)[NM], F(&fn)[NN]) {
                     if constexpr (decltype(next)::value)
-                    read(r, m1, w1, q, fm, fn);
-                else
-                    read(r, m0, w0, q, fm, fn);
+                        read(r, m1, w1, q, fm, fn);
+                    else
+                        read(r, m0, w0, q, fm, fn);
                 },
                 [&]() {
                     if (t + 2 == nk) {
@@ -768,13 +792,13 @@ __global__ void __launch_bounds__((DirectTile<BM, BN, WM, WN, __bf16>::NT))
                     ready(t + 2 - done);
                 },
                 [&](int c) { copy(c, m0, w0, t + 2 - done); }, [](const F(&)[NM]) {});
-            product_step<NM, NN, L::QA + L::QB>(
-                acc, f,
+            product_step<L::COPIES, 0, GRAD>(
+                acc, f, false,
                 [&](int r, auto next, int q, F(&fm)[NM], F(&fn)[NN]) {
                     if constexpr (decltype(next)::value)
-                    read(r, m0, w0, q, fm, fn);
-                else
-                    read(r, m1, w1, q, fm, fn);
+                        read(r, m0, w0, q, fm, fn);
+                    else
+                        read(r, m1, w1, q, fm, fn);
                 },
                 [&]() { ready(t + 3 - done); }, [&](int c) { copy(c, m1, w1, t + 3 - done); }, [](const F(&)[NM]) {});
         }
@@ -783,8 +807,9 @@ __global__ void __launch_bounds__((DirectTile<BM, BN, WM, WN, __bf16>::NT))
                                              again(lane));
         if (nxt.rows == 0) break;
         cur = nxt;
+        stored = !(GRAD && a.relu);  // (else loads are among the stores: all are waited for)
     }
-    wait_copies_barrier();  // (no copy outlives its workgroup)
+    wait_copies_barrier<0>();  // (no copy outlives its workgroup)
 }
 
 // ---------------------------------------------------------------------------
@@ -1041,20 +1066,20 @@ __global__ void __launch_bounds__((DirectTile<BM, BN, WM, WN, float>::NT))
         before(0);
         ready(0);
 #pragma unroll
-        for (int c = 0; c < L::QA + L::QB; ++c) copy(c, m0, w0);
+        for (int c = 0; c < L::COPIES; ++c) copy(c, m0, w0);
         before(1);
-        wait_copies_barrier();
         ready(1);
 #pragma unroll
-        for (int c = 0; c < L::QA + L::QB; ++c) copy(c, m1, w1);
-#pragma unroll
-        for (int r = 0; r < NM + NN; ++r) read(r, m0, w0, 0, f.m[0], f.n[0]);
+        for (int c = 0; c < L::COPIES; ++c) copy(c, m1, w1);
     }
+    wait_copies_barrier<L::COPIES>();
+#pragma unroll
+    for (int r = 0; r < NM + NN; ++r) read(r, m0, w0, 0, f.m[0], f.n[0]);
     // (steps past the last slot copy zeros)
     for (int t = 0; 64 * t < rows; t += 2) {
         before(t + 2);
-        product_step<NM, NN, L::QA + L::QB>(
-            acc, f,
+        product_step<L::COPIES, 0, true>(
+            acc, f, false,
             [&](int r, auto next, int q, F(&fm)[NM], F(&fn)[NN]) {
                 if constexpr (decltype(next)::value)
                     read(r, m1, w1, q, fm, fn);
@@ -1063,8 +1088,8 @@ __global__ void __launch_bounds__((DirectTile<BM, BN, WM, WN, float>::NT))
             },
             [&]() { ready(t + 2); }, [&](int c) { copy(c, m0, w0); }, bias);
         before(t + 3);
-        product_step<NM, NN, L::QA + L::QB>(
-            acc, f,
+        product_step<L::COPIES, 0, true>(
+            acc, f, false,
             [&](int r, auto next, int q, F(&fm)[NM], F(&fn)[NN]) {
                 if constexpr (decltype(next)::value)
                     read(r, m0, w0, q, fm, fn);
@@ -1073,9 +1098,10 @@ __global__ void __launch_bounds__((DirectTile<BM, BN, WM, WN, float>::NT))
             },
             [&]() { ready(t + 3); }, [&](int c) { copy(c, m1, w1); }, bias);
     }
-    wait_copies_barrier();
-    weights_epilogue<WM, WN>(a, w, (wave < NT / 128 ? m0 : m1) + wave % (NT / 128) * epilogue_bytes<float, WN>(), acc, bsum, w.m0 + wm * WM,
-                             w.n0 + wn * WN, with_bias, lane);
+    wait_copies_barrier<0>();
+    constexpr int HALF = NT / 128;  // waves whose rows leave through one stage
+    weights_epilogue<WM, WN>(a, w, (wave < HALF ? m0 : m1) + wave % HALF * epilogue_bytes<float, WN>(), acc, bsum,
+                             w.m0 + wm * WM, w.n0 + wn * WN, with_bias, lane);
 }
 
 // dW_e (and db_e) from the partial sums of its ranges, in their order.
@@ -1107,14 +1133,38 @@ void run_rows(const ExpertArgs& a, hipStream_t s) {
         <<<(unsigned)(tiles * n_tiles), RowsTile<T, GRAD, BM, BN, WM, WN>::NT, 0, s>>>(a, n_tiles);
 }
 
+// tile_rows <= BM slots a tile, `per_cu` workgroups on a CU.
 template <bool GRAD, int BM, int BN, int WM, int WN>
-void run_rows_direct(const ExpertArgs& a, hipStream_t s) {
+void run_rows_direct(const ExpertArgs& a, int tile_rows, int per_cu, hipStream_t s) {
     const int64_t N = GRAD ? a.d_in : a.d_out;
     const int n_tiles = (int)((N + BN - 1) / BN);
-    const int64_t tiles = (a.slots / BM + a.n_experts + 1) * n_tiles;
-    const unsigned blocks = (unsigned)(tiles < kCus ? (tiles + 7) / 8 * 8 : kCus);
+    const int64_t tiles = (a.slots / tile_rows + a.n_experts + 1) * n_tiles;
+    const unsigned blocks = (unsigned)(tiles < per_cu * kCus ? (tiles + 7) / 8 * 8 : per_cu * kCus);
     k_expert_rows_direct<GRAD, BM, BN, WM, WN>
-        <<<blocks, DirectTile<BM, BN, WM, WN, __bf16>::NT, 0, s>>>(a, n_tiles);
+        <<<blocks, DirectTile<BM, BN, WM, WN, __bf16>::NT, 0, s>>>(a, tile_rows, n_tiles);
+}
+
+// The least tile height, a multiple of 16, at which the tiles of 256 columns
+// still take no more rounds of the grid than at height 256; an expert's last
+// tile is taken to be half full.
+int tile_height(int64_t slots, int n_experts, int64_t n_tiles) {
+    const int64_t part = n_experts / 2;
+    const int64_t rounds = ((slots / 256 + part + 1) * n_tiles + kCus - 1) / kCus;
+    for (int h = 16; h < 256; h += 16)
+        if ((slots / h + part + 1) * n_tiles <= rounds * kCus) return h;
+    return 256;
+}
+
+template <bool GRAD>
+void pick_rows_direct(const ExpertArgs& a, hipStream_t s) {
+    const int64_t N = GRAD ? a.d_in : a.d_out;
+    const int h = tile_height(a.slots, a.n_experts, (N + 255) / 256);
+    if (h <= 128)
+        run_rows_direct<GRAD, 128, 128, 64, 64>(a, 128, 2, s);
+    else if (h <= 192)
+        run_rows_direct<GRAD, 192, 256, 96, 64>(a, h, 1, s);
+    else
+        run_rows_direct<GRAD, 256, 256, 128, 64>(a, h, 1, s);
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -1125,6 +1175,7 @@ bool direct_rows(const ExpertArgs& a, bool grad) {
     if (a.d_in % 8 || a.d_out % 8 || !aligned16(a.w)) return false;
     const int64_t ld = grad ? a.ld_dz : a.ld_x;
     if (ld % 8 || ld > 1 << 22) return false;  // (a tile of 256 such rows is within 2^31 bytes)
+    if (a.ld_y % 8 || a.ld_y > 1 << 22 || !aligned16(a.y)) return false;
     if (grad) return aligned16(a.dz);
     return aligned16(a.x) && (!a.order || a.x_rows * a.ld_x * 2 < kDirectBytes);
 }
@@ -1135,7 +1186,7 @@ void pick_rows(const ExpertArgs& a, hipStream_t s) {
     if (a.slots / a.n_experts < 64 || N <= 32)
         run_rows<T, GRAD, 32, 32, 32, 32>(a, s);
     else if (sizeof(T) == 2 && direct_rows(a, GRAD))
-        run_rows_direct<GRAD, NERF_RT>(a, s);
+        pick_rows_direct<GRAD>(a, s);
     else
         run_rows<T, GRAD, 128, 128, 64, 64>(a, s);
 }
@@ -1174,7 +1225,7 @@ void pick_weights(const ExpertArgs& a, hipStream_t s) {
     if (a.d_out <= 32 || a.d_in <= 32)
         run_weights<T, 32, 64, 32, 64>(a, s);
     else if (sizeof(T) == 2 && direct_weights(a))
-        run_weights_direct<NERF_WT>(a, s);
+        run_weights_direct<256, 256, 128, 64>(a, s);
     else
         run_weights<T, 128, 128, 64, 64>(a, s);
     if (a.chunk) {
