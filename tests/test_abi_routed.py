@@ -19,7 +19,7 @@ def _err(text=None):
 def test_workspace_sizes():
     assert B.nerf_route_workspace_size(100, 2, 8) == 0  # one workgroup sorts it
     nb = -(-262144 * 2 // 4096)
-    assert B.nerf_route_workspace_size(262144, 2, 8) == nb * 9 * 4
+    assert B.nerf_route_workspace_size(262144, 2, 8) == (nb + 1) * 9 * 4  # counts per workgroup, totals
     for bad in ((-1, 2, 8), (10, 0, 8), (10, 65, 8), (10, 2, 0), (10, 2, 4097), (1 << 31, 1, 8)):
         assert B.nerf_route_workspace_size(*bad) == 0
     assert B.nerf_distill_workspace_size(0, 100) == 0 and B.nerf_distill_workspace_size(10, 0) == 0

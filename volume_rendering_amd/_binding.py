@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import sys
 
 import numpy as np
 
@@ -162,6 +163,17 @@ def _ptr(t):
 def _stream(device=None):
     import torch
     return C.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+
+
+def _stream_handle() -> int:
+    """The current stream's handle, without the Stream object that
+    torch.cuda.current_stream() makes (2.7 us of a 7.5 us call) where torch
+    offers it."""
+    torch = _torch()
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is None:
+        return torch.cuda.current_stream().cuda_stream
+    return raw(torch.cuda.current_device())
 
 
 # ----------------------------------------------------------------------------
@@ -329,19 +341,25 @@ def nerf_hash_inr_train_step(x, target, grid: nerf_hashgrid, cfg: nerf_hash_inr_
 # Routed fields: samples to experts and back
 # ----------------------------------------------------------------------------
 
+def _torch():
+    return sys.modules["torch"]  # (the caller's tensors are torch's)
+
+
 def _tensor(t, what: str, dtype, shape, strided: bool = False) -> int:
     """Device pointer of ``t`` (0 for None) after checking type, shape and
     layout; ``strided``: a matrix whose rows may be further apart."""
     if t is None:
         return 0
+    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype != dtype:
         raise NerfError(f"{what}: dtype {t.dtype}, expected {dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise NerfError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if not t.is_cuda:
         raise NerfError(f"{what}: not a device tensor")
-    if not t.is_contiguous() and not (strided and t.dim() == 2 and (t.shape[1] == 1 or t.stride(1) == 1)
-                                      and (t.shape[0] <= 1 or t.stride(0) >= t.shape[1])):
+    if not (strided and t.dim() == 2 and (t.shape[1] == 1 or t.stride(1) == 1)
+            and (t.shape[0] <= 1 or t.stride(0) >= t.shape[1])):
         raise NerfError(f"{what}: {'rows' if strided else 'tensor'} must be contiguous")
     return t.data_ptr()
 
@@ -352,7 +370,7 @@ def _ld(t) -> int:
 
 
 def _dtype_of(t, what: str) -> int:
-    import torch
+    torch = _torch()
     if t.dtype == torch.bfloat16:
         return NERF_BF16
     if t.dtype == torch.float32:
@@ -378,47 +396,47 @@ def nerf_route_plan(ids, n_experts: int, offsets, order, place, workspace=None):
     """Sorts sample-expert pairs by expert: ``ids`` int32 [n, k] (a value
     outside [0, n_experts): no expert); writes int32 ``offsets``
     [n_experts + 1], ``order`` [n*k] and ``place`` [n, k]."""
-    import torch
+    torch = _torch()
     n, k = _matrix(ids, "ids")
     i32 = torch.int32
     ws, wsb = _ws(workspace)
     _check(lib().nerf_route_plan(_tensor(ids, "ids", i32, (n, k)), n, k, n_experts,
                                  _tensor(offsets, "offsets", i32, (n_experts + 1,)),
                                  _tensor(order, "order", i32, (n * k,)), _tensor(place, "place", i32, (n, k)), ws, wsb,
-                                 _stream()), "nerf_route_plan")
+                                 _stream_handle()), "nerf_route_plan")
 
 
 def nerf_route_gather(x, offsets, place, rows):
     """rows[place[t, j]] = x[t]: ``x`` [n, d] (rows may be strided), ``rows``
     [n*k, d]; rows of slots without an expert are zero."""
-    import torch
+    torch = _torch()
     n, k = _matrix(place, "place")
     d = _matrix(x, "x")[1]
     E, i32 = offsets.numel() - 1, torch.int32
     _check(lib().nerf_route_gather(_tensor(x, "x", x.dtype, (n, d), True), _dtype_of(x, "x"), _ld(x), n, k, d, E,
                                    _tensor(offsets, "offsets", i32, (E + 1,)), _tensor(place, "place", i32, (n, k)),
-                                   _tensor(rows, "rows", x.dtype, (n * k, d)), _stream()), "nerf_route_gather")
+                                   _tensor(rows, "rows", x.dtype, (n * k, d)), _stream_handle()), "nerf_route_gather")
 
 
 def nerf_route_combine(y, offsets, place, weights, out):
     """out[t] = sum_j weights[t, j] y[place[t, j]]: ``y`` [n*k, d], ``weights``
     float32 [n, k] or None (all 1), ``out`` [n, d] (rows may be strided).  With
     weights None it is the gradient of nerf_route_gather."""
-    import torch
+    torch = _torch()
     n, k = _matrix(place, "place")
     d = _matrix(y, "y")[1]
     E, i32 = offsets.numel() - 1, torch.int32
     _check(lib().nerf_route_combine(_tensor(y, "y", y.dtype, (n * k, d)), _dtype_of(y, "y"), n, k, d, E,
                                     _tensor(offsets, "offsets", i32, (E + 1,)), _tensor(place, "place", i32, (n, k)),
                                     _tensor(weights, "weights", torch.float32, (n, k)),
-                                    _tensor(out, "out", y.dtype, (n, d), True), _ld(out), _stream()),
+                                    _tensor(out, "out", y.dtype, (n, d), True), _ld(out), _stream_handle()),
            "nerf_route_combine")
 
 
 def nerf_route_combine_grad(dout, y, offsets, place, weights, dy, dweights=None):
     """Gradient of nerf_route_combine: ``dout`` [n, d] (rows may be strided),
     ``dy`` [n*k, d], ``dweights`` float32 [n, k] or None."""
-    import torch
+    torch = _torch()
     n, k = _matrix(place, "place")
     d = _matrix(y, "y")[1]
     E, i32, f32 = offsets.numel() - 1, torch.int32, torch.float32
@@ -428,7 +446,7 @@ def nerf_route_combine_grad(dout, y, offsets, place, weights, dy, dweights=None)
                                          _tensor(place, "place", i32, (n, k)),
                                          _tensor(weights, "weights", f32, (n, k)),
                                          _tensor(dy, "dy", y.dtype, (n * k, d)),
-                                         _tensor(dweights, "dweights", f32, (n, k)), _stream()),
+                                         _tensor(dweights, "dweights", f32, (n, k)), _stream_handle()),
            "nerf_route_combine_grad")
 
 
@@ -447,7 +465,7 @@ def nerf_expert_linear(x, weight, bias, offsets, y, order=None, k=1, relu=False)
     d_in], ``bias`` float32 [E, d_out] or None, ``y`` [slots, d_out]; ``x`` is
     [slots, d_in], or the samples' [n, d_in] rows with the plan's ``order`` and
     ``k``.  Rows of ``x`` and ``y`` may be strided."""
-    import torch
+    torch = _torch()
     L = _expert_layer(x, weight, _ld(y), order, k, relu)
     E, d_out, d_in = weight.shape
     slots, i32, dt = _matrix(y, "y")[0], torch.int32, weight.dtype
@@ -456,7 +474,7 @@ def nerf_expert_linear(x, weight, bias, offsets, y, order=None, k=1, relu=False)
                                     _tensor(bias, "bias", torch.float32, (E, d_out)),
                                     _tensor(offsets, "offsets", i32, (E + 1,)),
                                     _tensor(order, "order", i32, (slots,)),
-                                    slots, _tensor(y, "y", dt, (slots, d_out), True), _stream()),
+                                    slots, _tensor(y, "y", dt, (slots, d_out), True), _stream_handle()),
            "nerf_expert_linear")
 
 
@@ -470,7 +488,7 @@ def nerf_expert_linear_grad(dz, x, weight, offsets, dx=None, dweight=None, dbias
     before its activation): ``dx`` [slots, d_in] (zero where x <= 0 with
     ``relu_x``), float32 ``dweight`` [E, d_out, d_in] and ``dbias`` [E, d_out],
     each optional."""
-    import torch
+    torch = _torch()
     L = _expert_layer(x, weight, _ld(dz), order, k, relu_x)
     E, d_out, d_in = weight.shape
     slots, i32, dt, f32 = _matrix(dz, "dz")[0], torch.int32, weight.dtype, torch.float32
@@ -482,7 +500,7 @@ def nerf_expert_linear_grad(dz, x, weight, offsets, dx=None, dweight=None, dbias
                                          _tensor(order, "order", i32, (slots,)), slots,
                                          _tensor(dx, "dx", dt, (slots, d_in)),
                                          _tensor(dweight, "dweight", f32, weight.shape),
-                                         _tensor(dbias, "dbias", f32, (E, d_out)), ws, wsb, _stream()),
+                                         _tensor(dbias, "dbias", f32, (E, d_out)), ws, wsb, _stream_handle()),
            "nerf_expert_linear_grad")
 
 
@@ -491,7 +509,7 @@ def nerf_expert_linear_grad(dz, x, weight, offsets, dx=None, dweight=None, dbias
 # ----------------------------------------------------------------------------
 
 def _distill_args(logits, t_logits, t_ids, temperature, row_scale):
-    import torch
+    torch = _torch()
     n, classes = _matrix(logits, "logits")
     top = _matrix(t_ids, "t_ids")[1]
     return (_tensor(logits, "logits", logits.dtype, (n, classes), True), _dtype_of(logits, "logits"), _ld(logits), n,
@@ -510,19 +528,19 @@ def nerf_distill_topk(logits, t_logits, t_ids, temperature, loss, lse=None, grad
     [n, classes] against the teacher's largest: ``t_logits`` float32 and
     ``t_ids`` int32 [n, top].  Optional outputs: ``lse`` float32 [n] and
     ``grad`` [n, classes], scaled by ``row_scale`` (float32 [n])."""
-    import torch
+    torch = _torch()
     args = _distill_args(logits, t_logits, t_ids, temperature, row_scale)
     n, f32 = logits.shape[0], torch.float32
     ws, wsb = _ws(workspace)
     _check(lib().nerf_distill_topk(*args, _tensor(loss, "loss", f32, (n,)), _tensor(lse, "lse", f32, (n,)),
                                    _tensor(grad, "grad", logits.dtype, logits.shape, True), _ld(grad), ws, wsb,
-                                   _stream()), "nerf_distill_topk")
+                                   _stream_handle()), "nerf_distill_topk")
 
 
 def nerf_distill_topk_grad(logits, t_logits, t_ids, temperature, lse, grad, row_scale=None):
     """The gradient of nerf_distill_topk alone, from its ``lse``."""
-    import torch
+    torch = _torch()
     args = _distill_args(logits, t_logits, t_ids, temperature, row_scale)
     _check(lib().nerf_distill_topk_grad(*args, _tensor(lse, "lse", torch.float32, (logits.shape[0],)),
                                         _tensor(grad, "grad", logits.dtype, logits.shape, True), _ld(grad),
-                                        _stream()), "nerf_distill_topk_grad")
+                                        _stream_handle()), "nerf_distill_topk_grad")

@@ -180,6 +180,10 @@ __device__ __forceinline__ void mma(f32x16& acc, const typename Elt<T>::Frag& a,
 // Register-staged tile copies: any width, stride and alignment.  Elements past
 // the matrix are zero, so a step past k or a row past the group adds nothing.
 // ---------------------------------------------------------------------------
+// Two LDS stages; one in a workgroup of a single wave, which has nobody to wait
+// for and lives from many workgroups on a CU (k-steps are few there).
+constexpr int staged_stages(int NT) { return NT == 64 ? 1 : 2; }
+
 template <class T, int R, int NT>
 struct StageRows {  // R rows, k contiguous
     static constexpr int UNITS = R * 8, UPT = (UNITS + NT - 1) / NT;
@@ -345,10 +349,10 @@ __device__ __forceinline__ void rows_epilogue(const ExpertArgs& a, const Group& 
 // ---------------------------------------------------------------------------
 template <class T, bool GRAD, int BM, int BN, int WM, int WN>
 struct RowsTile {
-    static constexpr int NT = 64 * (BM / WM) * (BN / WN);
+    static constexpr int NT = 64 * (BM / WM) * (BN / WN), STAGES = staged_stages(NT);
     static constexpr int A_BYTES = BM * kStepBytes, STAGE = A_BYTES + BN * kStepBytes;
     static constexpr int EPI = (NT / 64) * epilogue_bytes<T, WN>();
-    static constexpr int LDS = 2 * STAGE > EPI ? 2 * STAGE : EPI;
+    static constexpr int LDS = STAGES * STAGE > EPI ? STAGES * STAGE : EPI;
 };
 
 template <class T, bool GRAD, int BM, int BN, int WM, int WN>
@@ -422,13 +426,94 @@ __global__ void __launch_bounds__((RowsTile<T, GRAD, BM, BN, WM, WN>::NT))
 #pragma unroll
                 for (int i = 0; i < WN / 32; ++i) mma<T>(acc[j][i], fn[i], fm[j]);
         }
-        if (more) store(lds + (buf ^ 1) * L::STAGE);
+        if (L::STAGES == 1) __syncthreads();
+        buf = L::STAGES == 1 ? 0 : buf ^ 1;
+        if (more) store(lds + buf * L::STAGE);
         __syncthreads();
-        buf ^= 1;
     }
 
     rows_epilogue<T, GRAD, WM, WN>(a, g, lds + wave * epilogue_bytes<T, WN>(), acc, y, rows, wm * WM, n0 + wn * WN, N,
                                    lane);
+}
+
+// ---------------------------------------------------------------------------
+// Forward for few slots (serving): bound by the read of the touched experts'
+// weights.  A workgroup owns 16 slots of an expert and 16 outputs; its four
+// waves take a quarter of k each, straight from memory to registers (each
+// weight is used once, so LDS would only add a step), eight loads in flight,
+// and their partial sums are added up in LDS in a fixed order.
+// Slots are found like tiles, or, with fewer slots than tiles, one workgroup
+// row per slot, of which those that start a tile work.
+// ---------------------------------------------------------------------------
+constexpr int kFewWaves = 4, kFewAhead = 8;
+constexpr int kFewSlots = 256;
+
+template <class T>
+__global__ void __launch_bounds__(64 * kFewWaves) k_expert_few(ExpertArgs a, int n_tiles, int by_slot) {
+    using IO = RowIO<T>;
+    constexpr int BK = 4 * IO::PER;  // k per load: four lane groups of a piece
+    __shared__ float part[kFewWaves][16][17];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int nt = blockIdx.x % n_tiles, v = blockIdx.x / n_tiles;
+    Group g;
+    if (by_slot) {
+        g.e = last_where(a.n_experts + 1, [&](int e) { return a.offsets[e] <= v; });
+        const int o0 = clamp_slot(a.offsets[g.e], a.slots);
+        const int o1 = g.e < a.n_experts ? clamp_slot(a.offsets[g.e + 1], a.slots) : (int)a.slots;
+        if (v < o0 || v >= o1 || (v - o0) % 16) return;
+        g.lo = v;
+        g.hi = o1 - v > 16 ? v + 16 : o1;
+    } else {
+        g = find_group(a, v, 16, a.n_experts + 1);
+    }
+    const int rows = g.hi - g.lo;
+    if (rows <= 0) return;
+    const int64_t K = a.d_in, N = a.d_out, n0 = 16 * (int64_t)nt;
+    if (g.e < a.n_experts) {
+        const int64_t n = n0 + (lane & 15);
+        const T* const w = (const T*)a.w + ((int64_t)g.e * N + (n < N ? n : N - 1)) * K;
+        const int64_t t = (lane & 15) < rows ? x_row(a, g.lo + (lane & 15)) : -1;
+        const T* const x = (const T*)a.x + (t < 0 ? 0 : t) * a.ld_x;
+        const int64_t per = (K + kFewWaves * BK - 1) / (kFewWaves * BK) * BK;
+        const int64_t k1 = (wave + 1) * per < K ? (wave + 1) * per : K;
+        f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int64_t k0 = wave * per; k0 < k1; k0 += kFewAhead * BK) {
+            typename IO::Vec fw[kFewAhead], fx[kFewAhead];
+#pragma unroll
+            for (int u = 0; u < kFewAhead; ++u) {
+                const int64_t k = k0 + u * BK + (lane >> 4) * IO::PER;
+                fw[u] = fx[u] = IO::zero();
+                if (k < k1) {
+                    fw[u] = IO::load(w, k, k1);
+                    if (t >= 0) fx[u] = IO::load(x, k, k1);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kFewAhead; ++u) {
+                if constexpr (sizeof(T) == 2)
+                    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, fx[u].u),
+                                                                  __builtin_bit_cast(bf16x8, fw[u].u), acc, 0, 0, 0);
+                else
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        acc = __builtin_amdgcn_mfma_f32_16x16x4f32(fx[u].e[j], fw[u].e[j], acc, 0, 0, 0);
+            }
+        }
+        // (a lane holds slots 4 (lane / 16) + r of output lane % 16)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) part[wave][4 * (lane >> 4) + r][lane & 15] = acc[r];
+    }
+    __syncthreads();
+    const int m = tid >> 4, n = tid & 15;
+    if (m >= rows || n0 + n >= N) return;
+    float y = 0.0f;
+    if (g.e < a.n_experts) {
+        if (a.bias) y = a.bias[(int64_t)g.e * N + n0 + n];
+#pragma unroll
+        for (int i = 0; i < kFewWaves; ++i) y += part[i][m][n];
+        if (a.relu && y < 0.0f) y = 0.0f;
+    }
+    ((T*)a.y)[(g.lo + m) * a.ld_y + n0 + n] = (T)y;
 }
 
 // ---------------------------------------------------------------------------
@@ -819,10 +904,10 @@ __global__ void __launch_bounds__((DirectTile<BM, BN, WM, WN, __bf16>::NT))
 // ---------------------------------------------------------------------------
 template <class T, int BM, int BN, int WM, int WN>
 struct WeightTile {
-    static constexpr int NT = 64 * (BM / WM) * (BN / WN);
+    static constexpr int NT = 64 * (BM / WM) * (BN / WN), STAGES = staged_stages(NT);
     static constexpr int A_BYTES = BM * kStepBytes, STAGE = A_BYTES + BN * kStepBytes;
     static constexpr int EPI = (NT / 64) * epilogue_bytes<float, WN>();
-    static constexpr int LDS = 2 * STAGE > EPI ? 2 * STAGE : EPI;
+    static constexpr int LDS = STAGES * STAGE > EPI ? STAGES * STAGE : EPI;
 };
 
 // The expert with the v-th most slots, for up to 64 experts (v beyond): the
@@ -977,13 +1062,14 @@ __global__ void __launch_bounds__((WeightTile<T, BM, BN, WM, WN>::NT))
                 for (int i = 0; i < WN / 32; ++i) mma<T>(acc[j][i], fn[i], fm[j]);
             if (with_bias) add_bias<T>(bsum, fm);
         }
+        if (L::STAGES == 1) __syncthreads();
+        buf = L::STAGES == 1 ? 0 : buf ^ 1;
         if (more) {
-            char* next = lds + (buf ^ 1) * L::STAGE;
+            char* next = lds + buf * L::STAGE;
             sa.store(next, tid);
             sb.store(next + L::A_BYTES, tid);
         }
         __syncthreads();
-        buf ^= 1;
     }
     weights_epilogue<WM, WN>(a, w, lds + wave * epilogue_bytes<float, WN>(), acc, bsum, w.m0 + wm * WM,
                              w.n0 + wn * WN, with_bias, lane);
@@ -1180,12 +1266,26 @@ bool direct_rows(const ExpertArgs& a, bool grad) {
     return aligned16(a.x) && (!a.order || a.x_rows * a.ld_x * 2 < kDirectBytes);
 }
 
+template <class T>
+void run_few(const ExpertArgs& a, hipStream_t s) {
+    const int n_tiles = (a.d_out + 15) / 16;
+    const int64_t tiles = a.slots / 16 + a.n_experts + 1;
+    const bool by_slot = a.slots < tiles;
+    k_expert_few<T><<<(unsigned)((by_slot ? a.slots : tiles) * n_tiles), 64 * kFewWaves, 0, s>>>(a, n_tiles, by_slot);
+}
+
 template <class T, bool GRAD>
 void pick_rows(const ExpertArgs& a, hipStream_t s) {
     const int64_t N = GRAD ? a.d_in : a.d_out;
-    if (a.slots / a.n_experts < 64 || N <= 32)
-        run_rows<T, GRAD, 32, 32, 32, 32>(a, s);
-    else if (sizeof(T) == 2 && direct_rows(a, GRAD))
+    const int64_t per = a.slots / a.n_experts;  // slots an expert has on average
+    if (!GRAD && a.slots <= kFewSlots && per < 16)
+        run_few<T>(a, s);
+    else if (per < 64 || N <= 32) {
+        if (N <= 32)
+            run_rows<T, GRAD, 32, 32, 32, 32>(a, s);
+        else
+            run_rows<T, GRAD, 32, 64, 32, 64>(a, s);
+    } else if (sizeof(T) == 2 && direct_rows(a, GRAD))
         pick_rows_direct<GRAD>(a, s);
     else
         run_rows<T, GRAD, 128, 128, 64, 64>(a, s);

@@ -18,17 +18,17 @@ enum ExpertCheckBit : unsigned {
 };
 
 // ---- routing (route.hip) ----
-// Pairs one workgroup sorts; the plan's workspace holds one row of E + 1
-// counts per workgroup.
+// Pairs one workgroup sorts; the plan's workspace holds a row of E + 1 counts
+// per workgroup and one of totals.
 constexpr int kRouteMaxExperts = 4096;
 constexpr int kRouteWaves = 8;
+constexpr int kRouteBatch = 8;  // pairs a lane holds in registers
 inline int64_t route_chunk(int64_t pairs) {
-    // 512 pairs a wave at least, so that its counters (cleared, summed and
-    // scanned per workgroup) cost less than its pairs; at most 256 workgroups,
-    // whose counts every workgroup reads
-    int64_t c = 64 * kRouteWaves * 8;
-    const int64_t per = (pairs + 255) / 256;
-    if (c < per) c = (per + 64 * kRouteWaves - 1) / (64 * kRouteWaves) * (64 * kRouteWaves);
+    // one batch a lane; beyond 2^22 pairs more, so that the counts of 1024
+    // workgroups stay a small part of what is read
+    int64_t c = 64 * kRouteWaves * kRouteBatch;
+    const int64_t per = (pairs + 1023) / 1024;
+    if (c < per) c = (per + c - 1) / c * c;
     return c;
 }
 inline int64_t route_blocks(int64_t pairs) { return (pairs + route_chunk(pairs) - 1) / route_chunk(pairs); }

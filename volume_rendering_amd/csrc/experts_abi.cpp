@@ -98,17 +98,17 @@ nerf_status check_layer(const char* who, const nerf_expert_layer* L, const int32
                  "%s: widths %d -> %d outside 1..%d", who, L->d_in, L->d_out, kMaxWidth);
     NERF_REQUIRE(L->ld_x == 0 || L->ld_x >= L->d_in, "%s: ld_x %lld below d_in", who, (long long)L->ld_x);
     NERF_REQUIRE(L->ld_y == 0 || L->ld_y >= L->d_out, "%s: ld_y %lld below d_out", who, (long long)L->ld_y);
-    // (kernels count k-steps of 64 slots in 32 bits, two past the end)
-    NERF_REQUIRE(slots >= 0 && slots <= kMaxPairs - 255, "%s: slots %lld", who, (long long)slots);
+    NERF_REQUIRE(slots >= 0 && slots <= kMaxPairs, "%s: slots %lld", who, (long long)slots);
     NERF_REQUIRE(L->x_rows >= 0 && (L->x_rows > 0 || !order || slots == 0), "%s: x_rows %lld", who,
                  (long long)L->x_rows);
     NERF_REQUIRE(!order || (L->k >= 1 && L->k <= NERF_MAX_CHOICES), "%s: k %d outside 1..%d", who, L->k,
                  NERF_MAX_CHOICES);
     if (L->n_experts > NERF_MAX_EXPERTS)
         return nerf_fail(NERF_ERR_UNSUPPORTED, "%s: n_experts %d above %d", who, L->n_experts, NERF_MAX_EXPERTS);
-    // the smallest tiles: 64 work items per 32 slots x 32 columns, or per 16 x 16 (few slots only)
+    // the smallest tiles: at most 256 work items per 32 slots x 32 columns
     const int64_t width = L->d_in > L->d_out ? L->d_in : L->d_out;
-    if ((slots / 32 + L->n_experts + 1) * ((width + 31) / 32) * 256 > kMaxItems)
+    // (and k-steps of 64 slots are counted in 32 bits, two past the end)
+    if (slots > kMaxPairs - 255 || (slots / 32 + L->n_experts + 1) * ((width + 31) / 32) * 256 > kMaxItems)
         return nerf_fail(NERF_ERR_UNSUPPORTED, "%s: %lld slots x %lld columns exceed one launch", who,
                          (long long)slots, (long long)width);
     return NERF_OK;
@@ -159,7 +159,7 @@ size_t nerf_route_workspace_size(int64_t n, int k, int n_experts) {
     if (n < 0 || k < 1 || k > NERF_MAX_CHOICES || n_experts < 1 || n_experts > NERF_MAX_EXPERTS || n > kMaxPairs / k)
         return 0;
     const int64_t nb = route_blocks(n * k);
-    return nb > 1 ? (size_t)nb * (size_t)(n_experts + 1) * sizeof(int32_t) : 0;
+    return nb > 1 ? (size_t)(nb + 1) * (size_t)(n_experts + 1) * sizeof(int32_t) : 0;
 }
 
 nerf_status nerf_route_plan(const int32_t* ids, int64_t n, int k, int n_experts, int32_t* offsets, int32_t* order,
