@@ -29,9 +29,11 @@ struct MaxSum {
     float m, s;
 };
 
-// 2^((x - m) c); with m = -inf every x is -inf (0) or NaN (x - x keeps it).
-__device__ __forceinline__ float exp2_below(float x, float m, float c) {
-    return m == -INFINITY ? (x == -INFINITY ? 0.0f : x - x) : __builtin_amdgcn_exp2f((x - m) * c);
+// What to subtract for the maximum m: with m = -inf every logit is -inf (or NaN)
+// and 2^((x - 0) c) is 0 (or NaN), as it has to be.
+__device__ __forceinline__ float shift_of(float m) { return m == -INFINITY ? 0.0f : m; }
+__device__ __forceinline__ float exp2_below(float x, float shift, float c) {
+    return __builtin_amdgcn_exp2f((x - shift) * c);
 }
 
 __device__ __forceinline__ MaxSum join(const MaxSum& a, const MaxSum& b, float c) {
@@ -74,8 +76,9 @@ __device__ __forceinline__ void add_piece(MaxSum& a, const typename RowIO<T>::Ve
         if (a.m != -INFINITY) a.s *= __builtin_amdgcn_exp2f((a.m - m) * c);
         a.m = m;
     }
+    const float shift = shift_of(a.m);
 #pragma unroll
-    for (int i = 0; i < RowIO<T>::PER; ++i) a.s += exp2_below(z[i], a.m, c);
+    for (int i = 0; i < RowIO<T>::PER; ++i) a.s += exp2_below(z[i], shift, c);
 }
 
 // Maximum and sum of classes [c0, c1) of a row, by NT threads.
@@ -172,33 +175,43 @@ struct TopLds {
 
 template <class T, int NT>
 __device__ __forceinline__ void patch_top(const DistillArgs& a, const TopLds& t, const T* row, T* grad, int64_t c0,
-                                          int64_t c1, float c, float m, float inv, float scale) {
+                                          int64_t c1, float c, float shift, float inv, float scale) {
     for (int j = threadIdx.x; j < a.top; j += NT) {
         const int id = t.id[j];
         if (id < 0 || id < c0 || id >= c1) continue;
         float p = 0.0f;
         for (int i = 0; i < a.top; ++i) p += t.id[i] == id ? t.p[i] : 0.0f;
-        const float q = exp2_below((float)row[id], m, c) * inv;
+        const float q = exp2_below((float)row[id], shift, c) * inv;
         grad[id] = (T)(scale * (t.total * q - p));
     }
 }
 
 template <class T, int NT>
 __device__ __forceinline__ void write_grad(const DistillArgs& a, const TopLds& t, const T* row, T* grad, int64_t c0,
-                                           int64_t c1, float c, float m, float inv, float scale) {
+                                           int64_t c1, float c, float shift, float inv, float scale) {
     constexpr int PER = RowIO<T>::PER;
     const float f = scale * t.total * inv;
+    const int64_t v0 = c0 + (int64_t)threadIdx.x * PER;
     // a row without entries has gradient 0 whatever its logits
-    const bool none = t.total == 0.0f;
-    for (int64_t v = c0 + (int64_t)threadIdx.x * PER; v < c1; v += NT * PER) {
-        const typename RowIO<T>::Vec x = RowIO<T>::load(row, v, c1);
+    if (__builtin_amdgcn_readfirstlane(t.total == 0.0f)) {
+        for (int64_t v = v0; v < c1; v += NT * PER) RowIO<T>::stream(grad, v, c1, RowIO<T>::zero());
+        return;
+    }
+    auto piece = [&](int64_t v, const typename RowIO<T>::Vec& x) {
         float g[PER];
 #pragma unroll
-        for (int i = 0; i < PER; ++i) g[i] = none ? 0.0f : f * exp2_below(RowIO<T>::get(x, i), m, c);
-        RowIO<T>::store(grad, v, c1, RowIO<T>::pack(g));
+        for (int i = 0; i < PER; ++i) g[i] = f * exp2_below(RowIO<T>::get(x, i), shift, c);
+        RowIO<T>::stream(grad, v, c1, RowIO<T>::pack(g));  // (the row's logits stay in the cache for this sweep)
+    };
+    int64_t v = v0;
+    for (; v + NT * PER + PER <= c1; v += 2 * NT * PER) {  // two loads in flight
+        const typename RowIO<T>::Vec x0 = RowIO<T>::load(row, v, c1), x1 = RowIO<T>::load(row, v + NT * PER, c1);
+        piece(v, x0);
+        piece(v + NT * PER, x1);
     }
+    for (; v < c1; v += NT * PER) piece(v, RowIO<T>::load(row, v, c1));
     __syncthreads();
-    if (!none) patch_top<T, NT>(a, t, row, grad, c0, c1, c, m, inv, scale);
+    patch_top<T, NT>(a, t, row, grad, c0, c1, c, shift, inv, scale);
 }
 
 template <class T>
@@ -240,7 +253,7 @@ __global__ void __launch_bounds__(NT) k_distill_rows(DistillArgs a) {
     if (!a.grad) return;
     __syncthreads();
     const float scale = a.temperature * (a.row_scale ? a.row_scale[r] : 1.0f);
-    write_grad<T, NT>(a, top, row, (T*)a.grad + r * a.ld_grad, 0, a.classes, c, v.m,
+    write_grad<T, NT>(a, top, row, (T*)a.grad + r * a.ld_grad, 0, a.classes, c, shift_of(v.m),
                       v.s == 0.0f ? 0.0f : 1.0f / v.s, scale);
 }
 
@@ -306,7 +319,7 @@ __global__ void __launch_bounds__(kSplitThreads) k_distill_join(DistillArgs a, i
     int64_t c0, c1;
     split_range(a.classes, gsplits, i, c0, c1);
     const float scale = a.temperature * (a.row_scale ? a.row_scale[r] : 1.0f);
-    write_grad<T, kSplitThreads>(a, top, row, (T*)a.grad + r * a.ld_grad, c0, c1, kLog2e / a.temperature, all.m,
+    write_grad<T, kSplitThreads>(a, top, row, (T*)a.grad + r * a.ld_grad, c0, c1, kLog2e / a.temperature, shift_of(all.m),
                                  all.s == 0.0f ? 0.0f : 1.0f / all.s, scale);
 }
 
@@ -322,7 +335,7 @@ __global__ void __launch_bounds__(kSplitThreads) k_distill_grad(DistillArgs a, i
     split_range(a.classes, gsplits, i, c0, c1);
     const float scale = a.temperature * (a.row_scale ? a.row_scale[r] : 1.0f);
     write_grad<T, kSplitThreads>(a, top, (const T*)a.logits + r * a.ld, (T*)a.grad + r * a.ld_grad, c0, c1,
-                                 kLog2e / a.temperature, a.lse[r] * a.temperature, 1.0f, scale);
+                                 kLog2e / a.temperature, shift_of(a.lse[r] * a.temperature), 1.0f, scale);
 }
 
 // Workgroups per row of a gradient sweep: ranges of 16384 classes.
@@ -337,8 +350,10 @@ void run_distill(const DistillArgs& a, hipStream_t s) {
         k_distill_join<T><<<(unsigned)(a.n * gs), kSplitThreads, 0, s>>>(a, splits, gs);
     } else if (a.classes <= 2048) {
         k_distill_rows<T, 64><<<(unsigned)a.n, 64, 0, s>>>(a);
-    } else {
+    } else if (a.classes * sizeof(T) <= 65536) {
         k_distill_rows<T, 256><<<(unsigned)a.n, 256, 0, s>>>(a);
+    } else {
+        k_distill_rows<T, 1024><<<(unsigned)a.n, 1024, 0, s>>>(a);
     }
 }
 

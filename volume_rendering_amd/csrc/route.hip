@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(kRowThreads) k_route_gather(RouteRows r) {
                 const int slot = pl[j];
                 NERF_DCHECK(slot >= 0 && slot < r.n * r.k, kCheckRouteSlot);
                 if ((unsigned)slot >= (uint64_t)(r.n * r.k)) continue;
-                IO::store((T*)r.out + (int64_t)slot * r.d, p.c, r.d, slot < live ? v : IO::zero());
+                IO::stream((T*)r.out + (int64_t)slot * r.d, p.c, r.d, slot < live ? v : IO::zero());
             }
         }
     }
@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(kRowThreads) k_route_combine(RouteRows r) {
 #pragma unroll
                         for (int i = 0; i < IO::PER; ++i) acc[i] = fmaf(wj[u], IO::get(v[u], i), acc[i]);
             }
-            IO::store((T*)r.out + t * r.ldo, p.c, r.d, IO::pack(acc));
+            IO::stream((T*)r.out + t * r.ldo, p.c, r.d, IO::pack(acc));
         }
     }
 }
@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(kRowThreads) k_route_combine_grad(RouteRows r)
                         // (columns past d are zero in both, those of the previous piece are counted there)
                         if (used[u] && i >= p.skip) dot[u] = fmaf(f, IO::get(y[u], i), dot[u]);
                     }
-                    IO::store((T*)r.out + row[u], p.c, r.d, IO::pack(o));
+                    IO::stream((T*)r.out + row[u], p.c, r.d, IO::pack(o));
                 }
             }
             if (r.dweights)

@@ -9,6 +9,7 @@
 namespace nerf {
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4_loose __attribute__((ext_vector_type(4), aligned(2)));
 
 template <class T>
 struct RowIO {
@@ -43,6 +44,14 @@ struct RowIO {
 #pragma unroll
             for (int i = 0; i < PER; ++i)
                 if (c + i < width) row[c + i] = v.e[i];
+    }
+    // A store that is not to be read again soon: it leaves the caches to data
+    // that is (nontemporal).
+    static __device__ __forceinline__ void stream(T* row, int64_t c, int64_t width, const Vec& v) {
+        if (c + PER <= width)
+            __builtin_nontemporal_store(v.u, reinterpret_cast<u32x4_loose*>(row + c));
+        else
+            store(row, c, width, v);
     }
     static __device__ __forceinline__ float get(const Vec& v, int i) { return (float)v.e[i]; }
     static __device__ __forceinline__ Vec pack(const float (&f)[PER]) {
