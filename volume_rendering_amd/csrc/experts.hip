@@ -336,7 +336,7 @@ __device__ __forceinline__ void rows_epilogue(const ExpertArgs& a, const Group& 
                 }
                 if constexpr (DIRECT)
                     __builtin_amdgcn_raw_buffer_store_b128(
-                        v.u, ry, in ? (uint32_t)((r * a.ld_y + nw + n) * (int)sizeof(T)) : kBufferOutOfRange, 0, 0);
+                        v.u, ry, in ? (uint32_t)((r * a.ld_y + nw + n) * (int)sizeof(T)) : kBufferOutOfRange, 0, 2);
                 else
                     RowIO<T>::store(y + (int64_t)r * a.ld_y, nw + n, N, v);
             });
@@ -1274,18 +1274,30 @@ void run_few(const ExpertArgs& a, hipStream_t s) {
     k_expert_few<T><<<(unsigned)((by_slot ? a.slots : tiles) * n_tiles), 64 * kFewWaves, 0, s>>>(a, n_tiles, by_slot);
 }
 
+// Which rows kernel, by the slots an expert has on average (all bfloat16
+// figures are of one call, us):
+//  - below 16, for at most 256 slots: k_expert_few.  16 experts 1024 -> 4096, 64
+//    slots: 31 against 35 with 32-slot tiles (float32, 1024 -> 2048: 37 against
+//    64); 256 slots, 16 an expert: 49 against 38; 1024 slots, 4 an expert: 14
+//    against 12.
+//  - below 32: 32-slot tiles.  1024 experts 256 -> 256, 16 slots each: 42 against
+//    51 with copied tiles; 64 experts 512 -> 512, 32 each: 18 against 16.
+//  - also below 256 with more than 63 experts (whose tiles have to be searched
+//    for) and at most 128 x 128 weights: 1024 experts, 64 slots each, 64 -> 64: 15
+//    against 43, 128 -> 128: 29 against 45, 256 -> 256: 76 against 71; 256 slots
+//    each, 128 -> 128: 79 against 79.
+//  - else copied tiles where rows allow it, or staged ones.
 template <class T, bool GRAD>
 void pick_rows(const ExpertArgs& a, hipStream_t s) {
-    const int64_t N = GRAD ? a.d_in : a.d_out;
-    const int64_t per = a.slots / a.n_experts;  // slots an expert has on average
+    const int64_t N = GRAD ? a.d_in : a.d_out, per = a.slots / a.n_experts;
+    const bool narrow = a.n_experts > 63 && (int64_t)a.d_in * a.d_out <= 128 * 128;
     if (!GRAD && a.slots <= kFewSlots && per < 16)
         run_few<T>(a, s);
-    else if (per < 64 || N <= 32) {
-        if (N <= 32)
-            run_rows<T, GRAD, 32, 32, 32, 32>(a, s);
-        else
-            run_rows<T, GRAD, 32, 64, 32, 64>(a, s);
-    } else if (sizeof(T) == 2 && direct_rows(a, GRAD))
+    else if (N <= 32)
+        run_rows<T, GRAD, 32, 32, 32, 32>(a, s);
+    else if (per < (narrow ? 256 : 32))
+        run_rows<T, GRAD, 32, 64, 32, 64>(a, s);
+    else if (sizeof(T) == 2 && direct_rows(a, GRAD))
         pick_rows_direct<GRAD>(a, s);
     else
         run_rows<T, GRAD, 128, 128, 64, 64>(a, s);
@@ -1320,14 +1332,25 @@ bool direct_weights(const ExpertArgs& a) {
     return aligned16(a.x) && aligned16(a.dz) && (!a.order || a.x_rows * a.ld_x * 2 < kDirectBytes);
 }
 
+// 256 x 256 tiles of a weight gradient where an expert's sums are long (2048
+// slots and more on average), else 128 x 128 (two workgroups on a CU).  Both
+// gradients of 16 experts 1024 -> 4096, 2048 slots each: 626 us against 690;
+// 64 experts 512 -> 512, 512 slots each: 115 against 100; 8 experts 256 -> 256,
+// 512 slots each: 36 against 27.
+bool wide_weight_tiles(int64_t slots, int n_experts, int d_in, int d_out) {
+    return slots / n_experts >= 2048 && d_in > 128 && d_out > 128;
+}
+
 template <class T>
 void pick_weights(const ExpertArgs& a, hipStream_t s) {
     if (a.d_out <= 32 || a.d_in <= 32)
         run_weights<T, 32, 64, 32, 64>(a, s);
-    else if (sizeof(T) == 2 && direct_weights(a))
+    else if (sizeof(T) == 4 || !direct_weights(a))
+        run_weights<T, 128, 128, 64, 64>(a, s);
+    else if (wide_weight_tiles(a.slots, a.n_experts, a.d_in, a.d_out))
         run_weights_direct<256, 256, 128, 64>(a, s);
     else
-        run_weights<T, 128, 128, 64, 64>(a, s);
+        run_weights_direct<128, 128, 64, 64>(a, s);
     if (a.chunk) {
         const int64_t per = (int64_t)a.d_out * a.d_in + (a.db ? a.d_out : 0);
         k_expert_sum<<<dim3((unsigned)((per + 255) / 256), a.n_experts), 256, 0, s>>>(a);
@@ -1336,10 +1359,17 @@ void pick_weights(const ExpertArgs& a, hipStream_t s) {
 
 }  // namespace
 
+// With fewer tiles than half the workgroups that fit on the card, experts' slots
+// are split into ranges so that the items fill it once; every range costs a
+// write and a read of a float32 weight gradient, so none is below 512 slots.
 int64_t expert_grad_chunk(int64_t slots, int n_experts, int d_in, int d_out) {
-    const int64_t tiles = (int64_t)n_experts * ((d_in + 127) / 128) * ((d_out + 127) / 128);
-    if (tiles >= 512 || slots <= 2048) return 0;
-    return 2048;
+    const bool wide = wide_weight_tiles(slots, n_experts, d_in, d_out);
+    const int64_t side = wide ? 256 : 128, fit = wide ? kCus : 2 * kCus;
+    const int64_t tiles = ((d_in + side - 1) / side) * ((d_out + side - 1) / side);
+    if (n_experts * tiles >= fit / 2 || slots <= 1024) return 0;
+    const int64_t items = fit / tiles - n_experts > 1 ? fit / tiles - n_experts : 1;
+    const int64_t chunk = ((slots + items - 1) / items + 63) / 64 * 64;
+    return chunk > 512 ? chunk : 512;
 }
 
 void launch_expert_linear(bool bf16, const ExpertArgs& a, hipStream_t s) {
