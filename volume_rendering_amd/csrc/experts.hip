@@ -179,34 +179,62 @@ __device__ __forceinline__ void mma(f32x16& acc, const typename Elt<T>::Frag& a,
 // ---------------------------------------------------------------------------
 // Register-staged tile copies: any width, stride and alignment.  Elements past
 // the matrix are zero, so a step past k or a row past the group adds nothing.
+// A row's last, partial piece is loaded as the last whole one and shifted into
+// place when it goes to LDS: loads then hold nothing that waits for one.
 // ---------------------------------------------------------------------------
 // Two LDS stages; one in a workgroup of a single wave, which has nobody to wait
 // for and lives from many workgroups on a CU (k-steps are few there).
 constexpr int staged_stages(int NT) { return NT == 64 ? 1 : 2; }
 
+// Elements c .. of a row of `width`, to be settled (below) before use.
+template <class T>
+__device__ __forceinline__ typename RowIO<T>::Vec load_ahead(const T* row, int64_t c, int64_t width) {
+    if (width < RowIO<T>::PER) return RowIO<T>::load(row, c, width);  // (the same for every lane)
+    return RowIO<T>::load_whole(row + (c + RowIO<T>::PER <= width ? c : width - RowIO<T>::PER));
+}
+template <class T>
+__device__ __forceinline__ u32x4 settle(const typename RowIO<T>::Vec& v, int64_t c, int64_t width) {
+    const int64_t past = c + RowIO<T>::PER - width;
+    u32x4 u = v.u;
+    if (past > 0 && width >= RowIO<T>::PER) {
+        uint64_t lo = (uint64_t)u[1] << 32 | u[0], hi = (uint64_t)u[3] << 32 | u[2];
+        const int s = past < RowIO<T>::PER ? (int)past * 8 * (int)sizeof(T) : 128;  // bits of earlier elements
+        const uint64_t over = s < 64 ? hi << (64 - s) : 0;                           // (s is at least 16)
+        lo = s < 64 ? lo >> s | over : s < 128 ? hi >> (s - 64) : 0;
+        hi = s < 64 ? hi >> s : 0;
+        u = u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+    }
+    return u;
+}
+
 template <class T, int R, int NT>
 struct StageRows {  // R rows, k contiguous
     static constexpr int UNITS = R * 8, UPT = (UNITS + NT - 1) / NT;
+    const T* row[UPT];  // of each unit; NULL: a zero row
     typename RowIO<T>::Vec v[UPT];
-    // row_of(r): pointer to row r, or NULL (a zero row)
+    // row_of(r): pointer to row r, or NULL
     template <class F>
-    __device__ __forceinline__ void load(F&& row_of, int64_t k0, int64_t K, int tid) {
+    __device__ __forceinline__ void init(F&& row_of, int tid) {
 #pragma unroll
         for (int q = 0; q < UPT; ++q) {
             const int u = tid + NT * q;
-            v[q] = RowIO<T>::zero();
-            if (UNITS % NT == 0 || u < UNITS) {
-                const T* p = row_of(u >> 3);
-                if (p) v[q] = RowIO<T>::load(p, k0 + (u & 7) * RowIO<T>::PER, K);
-            }
+            row[q] = UNITS % NT == 0 || u < UNITS ? row_of(u >> 3) : nullptr;
         }
     }
-    __device__ __forceinline__ void store(char* tile, int tid) const {
+    __device__ __forceinline__ void load(int64_t k0, int64_t K, int tid) {
+#pragma unroll
+        for (int q = 0; q < UPT; ++q) {
+            v[q] = RowIO<T>::zero();
+            if (row[q]) v[q] = load_ahead<T>(row[q], k0 + ((tid + NT * q) & 7) * RowIO<T>::PER, K);
+        }
+    }
+    __device__ __forceinline__ void store(char* tile, int64_t k0, int64_t K, int tid) const {
 #pragma unroll
         for (int q = 0; q < UPT; ++q) {
             const int u = tid + NT * q, r = u >> 3;
             if (UNITS % NT == 0 || u < UNITS)
-                *reinterpret_cast<u32x4*>(tile + r * kStepBytes + (((u & 7) ^ swz_row(r)) << 4)) = v[q].u;
+                *reinterpret_cast<u32x4*>(tile + r * kStepBytes + (((u & 7) ^ swz_row(r)) << 4)) =
+                    settle<T>(v[q], k0 + (u & 7) * RowIO<T>::PER, K);
         }
     }
 };
@@ -214,27 +242,25 @@ struct StageRows {  // R rows, k contiguous
 template <class T, int C, int NT>
 struct StageCols {  // one k-step of a k-major matrix, C columns
     static constexpr int PIECES = C / RowIO<T>::PER, UNITS = Elt<T>::BK * PIECES, UPT = (UNITS + NT - 1) / NT;
+    static_assert(UNITS % NT == 0, "whole units");
     typename RowIO<T>::Vec v[UPT];
-    // row_of(k): pointer to the matrix row at k of this step, or NULL
+    static __device__ __forceinline__ int k_of(int q, int tid) { return (tid + NT * q) / PIECES; }
+    // row_of(q): pointer to the matrix row at unit q's k of this step, or NULL
     template <class F>
     __device__ __forceinline__ void load(F&& row_of, int64_t c0, int64_t width, int tid) {
 #pragma unroll
         for (int q = 0; q < UPT; ++q) {
-            const int u = tid + NT * q;
             v[q] = RowIO<T>::zero();
-            if (UNITS % NT == 0 || u < UNITS) {
-                const T* p = row_of(u / PIECES);
-                if (p) v[q] = RowIO<T>::load(p, c0 + (u % PIECES) * RowIO<T>::PER, width);
-            }
+            const T* p = row_of(q);
+            if (p) v[q] = load_ahead<T>(p, c0 + ((tid + NT * q) % PIECES) * RowIO<T>::PER, width);
         }
     }
-    __device__ __forceinline__ void store(char* tile, int tid) const {
+    __device__ __forceinline__ void store(char* tile, int64_t c0, int64_t width, int tid) const {
 #pragma unroll
         for (int q = 0; q < UPT; ++q) {
-            const int u = tid + NT * q, k = u / PIECES;
-            if (UNITS % NT == 0 || u < UNITS)
-                *reinterpret_cast<u32x4*>(tile + k * (C * (int)sizeof(T)) + (((u % PIECES) ^ swz_k<T, C>(k)) << 4)) =
-                    v[q].u;
+            const int u = tid + NT * q, k = u / PIECES, c = u % PIECES;
+            *reinterpret_cast<u32x4*>(tile + k * (C * (int)sizeof(T)) + ((c ^ swz_k<T, C>(k)) << 4)) =
+                settle<T>(v[q], c0 + c * RowIO<T>::PER, width);
         }
     }
 };
@@ -345,7 +371,15 @@ __device__ __forceinline__ void rows_epilogue(const ExpertArgs& a, const Group& 
 
 // ---------------------------------------------------------------------------
 // Forward and input gradient: a workgroup owns BM slots of one expert and BN
-// columns.  GRAD: weights are read k-major (k = outputs), rows are dz.
+// columns.  GRAD: weights are read k-major (k = outputs), rows are dz.  This
+// kernel serves every type, width, stride and alignment.  128 x 128 tiles: 8
+// experts 1024 -> 1024, 16,384 slots, float32: 384 us, 90 TF/s (a library product
+// of 4096 cubed: 142), two waves a SIMD being too few to hide each other's
+// barriers; 32 experts 333 -> 517, 131,072 slots, bfloat16: 201 us, 225 TF/s,
+// bound by the copies through registers.  32-slot tiles (one wave each) are bound
+// by the latency of one chain of load, store, read and multiplication, of which a
+// CU runs many side by side: 90,000 slots of 4096 experts 63 -> 32, float32, the
+// input gradient 30 us.
 // ---------------------------------------------------------------------------
 template <class T, bool GRAD, int BM, int BN, int WM, int WN>
 struct RowsTile {
@@ -379,33 +413,40 @@ __global__ void __launch_bounds__((RowsTile<T, GRAD, BM, BN, WM, WN>::NT))
     StageRows<T, BM, NT> sa;
     StageRows<T, BN, NT> sb;  // forward: rows of W
     StageCols<T, BN, NT> sc;  // gradient: W is k-major
+    sa.init(
+        [&](int r) -> const T* {
+            if (r >= rows) return nullptr;
+            if (GRAD) return (const T*)a.dz + (g.lo + r) * a.ld_dz;
+            const int64_t t = x_row(a, g.lo + r);
+            return t < 0 ? nullptr : (const T*)a.x + t * a.ld_x;
+        },
+        tid);
+    if constexpr (!GRAD) sb.init([&](int r) { return n0 + r < N ? w + (n0 + r) * K : nullptr; }, tid);
     auto load = [&](int64_t k0) {
-        sa.load(
-            [&](int r) -> const T* {
-                if (r >= rows) return nullptr;
-                if (GRAD) return (const T*)a.dz + (g.lo + r) * a.ld_dz;
-                const int64_t t = x_row(a, g.lo + r);
-                return t < 0 ? nullptr : (const T*)a.x + t * a.ld_x;
-            },
-            k0, K, tid);
+        sa.load(k0, K, tid);
         if constexpr (GRAD)
-            sc.load([&](int k) { return k0 + k < K ? w + (k0 + k) * N : nullptr; }, n0, N, tid);
+            sc.load(
+                [&](int q) {
+                    const int64_t k = k0 + sc.k_of(q, tid);
+                    return k < K ? w + k * N : nullptr;
+                },
+                n0, N, tid);
         else
-            sb.load([&](int r) { return n0 + r < N ? w + (n0 + r) * K : nullptr; }, k0, K, tid);
+            sb.load(k0, K, tid);
     };
-    auto store = [&](char* stage) {
-        sa.store(stage, tid);
+    auto store = [&](char* stage, int64_t k0) {
+        sa.store(stage, k0, K, tid);
         if constexpr (GRAD)
-            sc.store(stage + L::A_BYTES, tid);
+            sc.store(stage + L::A_BYTES, n0, N, tid);
         else
-            sb.store(stage + L::A_BYTES, tid);
+            sb.store(stage + L::A_BYTES, k0, K, tid);
     };
 
     f32x16 acc[WM / 32][WN / 32];
     rows_start<GRAD, WM, WN>(a, g.e, acc, n0 + wn * WN, N, lane);
 
     load(0);
-    store(lds);
+    store(lds, 0);
     __syncthreads();
     int buf = 0;
     for (int64_t k0 = 0; k0 < K; k0 += Elt<T>::BK) {
@@ -428,7 +469,7 @@ __global__ void __launch_bounds__((RowsTile<T, GRAD, BM, BN, WM, WN>::NT))
         }
         if (L::STAGES == 1) __syncthreads();
         buf = L::STAGES == 1 ? 0 : buf ^ 1;
-        if (more) store(lds + buf * L::STAGE);
+        if (more) store(lds + buf * L::STAGE, k0 + Elt<T>::BK);
         __syncthreads();
     }
 
@@ -438,7 +479,8 @@ __global__ void __launch_bounds__((RowsTile<T, GRAD, BM, BN, WM, WN>::NT))
 
 // ---------------------------------------------------------------------------
 // Forward for few slots (serving): bound by the read of the touched experts'
-// weights.  A workgroup owns 16 slots of an expert and 16 outputs; its four
+// weights, and for one sample by launch and latency (1024 -> 4096 bfloat16
+// through two experts: 16.8 MB, 3.4 us at 4.9 TB/s, 8.5 us a call).  A workgroup owns 16 slots of an expert and 16 outputs; its four
 // waves take a quarter of k each, straight from memory to registers (each
 // weight is used once, so LDS would only add a step), eight loads in flight,
 // and their partial sums are added up in LDS in a fixed order.
@@ -730,6 +772,15 @@ struct TileWalk {
     }
 };
 
+// Bound by the matrix cores and what feeds them from LDS.  16 experts
+// 1024 -> 4096, 32,768 slots: 294 us, 930 TF/s.  Of these the multiplications
+// alone take 175 us (copies of the kernel with the rest taken out), with the
+// fragments' reads 210, with the stores 233; the copies into LDS, which share
+// its ports, bring the rest, and 8.5 tiles a CU run as 9.  A library product of
+// 4096 x 4096 x 4096 without routing reaches 1320 TF/s here.  256 x 256 tiles of
+// four 128 x 64 waves read least from LDS a multiplication; fewer rows a tile
+// where that fills the last round of the grid (tile_height).
+// 8 experts 256 -> 256, 262,144 slots: 74 us, bound by memory (268 MB, 55 us).
 template <bool GRAD, int BM, int BN, int WM, int WN>
 __global__ void __launch_bounds__((DirectTile<BM, BN, WM, WN, __bf16>::NT))
     k_expert_rows_direct(ExpertArgs a, int tile_rows, int n_tiles) {
@@ -901,6 +952,11 @@ __global__ void __launch_bounds__((DirectTile<BM, BN, WM, WN, __bf16>::NT))
 // Weight gradient: k runs over an expert's slots, both operands are k-major.
 // A workgroup owns BM outputs x BN inputs of one expert and, with a.chunk,
 // one range of its slots (partial sums, added in order by k_expert_sum).
+// This kernel serves every type, width, stride and alignment; which rows of x a
+// step copies is read a step ahead.  16 experts 512 -> 512, 32,768 slots, float32:
+// 276 us, 62 TF/s; 32 experts 333 -> 517, 131,072 slots, bfloat16: 480 us, 94 TF/s;
+// 4096 experts 63 -> 32, 90,000 slots, float32: 29 us.  All bound by latency, as
+// k_expert_rows.
 // ---------------------------------------------------------------------------
 template <class T, int BM, int BN, int WM, int WN>
 struct WeightTile {
@@ -1023,31 +1079,45 @@ __global__ void __launch_bounds__((WeightTile<T, BM, BN, WM, WN>::NT))
 
     StageCols<T, BM, NT> sa;
     StageCols<T, BN, NT> sb;
+    int64_t from[sb.UPT];  // the next step's rows of x (-1: none), read a step ahead
+    auto before = [&](int64_t s0) {
+#pragma unroll
+        for (int q = 0; q < sb.UPT; ++q) {
+            const int64_t s = s0 + sb.k_of(q, tid);
+            from[q] = s < g.hi ? x_row(a, s) : -1;
+        }
+    };
     auto load = [&](int64_t s0) {
-        sa.load([&](int k) { return s0 + k < g.hi ? (const T*)a.dz + (s0 + k) * a.ld_dz : nullptr; }, w.m0, a.d_out,
-                tid);
-        sb.load(
-            [&](int k) -> const T* {
-                if (s0 + k >= g.hi) return nullptr;
-                const int64_t t = x_row(a, s0 + k);
-                return t < 0 ? nullptr : (const T*)a.x + t * a.ld_x;
+        sa.load(
+            [&](int q) {
+                const int64_t s = s0 + sa.k_of(q, tid);
+                return s < g.hi ? (const T*)a.dz + s * a.ld_dz : nullptr;
             },
-            w.n0, a.d_in, tid);
+            w.m0, a.d_out, tid);
+        sb.load([&](int q) { return from[q] < 0 ? nullptr : (const T*)a.x + from[q] * a.ld_x; }, w.n0, a.d_in, tid);
+    };
+    auto store = [&](char* stage) {
+        sa.store(stage, w.m0, a.d_out, tid);
+        sb.store(stage + L::A_BYTES, w.n0, a.d_in, tid);
     };
     f32x16 acc[WM / 32][WN / 32];
     float bsum[WM / 32] = {};
     clear(acc);
 
     if (g.lo < g.hi) {
+        before(g.lo);
         load(g.lo);
-        sa.store(lds, tid);
-        sb.store(lds + L::A_BYTES, tid);
+        before(g.lo + BK);
+        store(lds);
     }
     __syncthreads();
     int buf = 0;
     for (int64_t s0 = g.lo; s0 < g.hi; s0 += BK) {
         const bool more = s0 + BK < g.hi;
-        if (more) load(s0 + BK);
+        if (more) {
+            load(s0 + BK);
+            before(s0 + 2 * BK);
+        }
         const char *ta = lds + buf * L::STAGE, *tb = ta + L::A_BYTES;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -1064,11 +1134,7 @@ __global__ void __launch_bounds__((WeightTile<T, BM, BN, WM, WN>::NT))
         }
         if (L::STAGES == 1) __syncthreads();
         buf = L::STAGES == 1 ? 0 : buf ^ 1;
-        if (more) {
-            char* next = lds + buf * L::STAGE;
-            sa.store(next, tid);
-            sb.store(next + L::A_BYTES, tid);
-        }
+        if (more) store(lds + buf * L::STAGE);
         __syncthreads();
     }
     weights_epilogue<WM, WN>(a, w, lds + wave * epilogue_bytes<float, WN>(), acc, bsum, w.m0 + wm * WM,
@@ -1076,6 +1142,10 @@ __global__ void __launch_bounds__((WeightTile<T, BM, BN, WM, WN>::NT))
 }
 
 // The same with direct copies (bfloat16).  THROUGH: x rows through the order.
+// Bound like k_expert_rows_direct; both operands are read transposed, which
+// takes two LDS reads a fragment: 16 experts 1024 -> 4096, 32,768 slots: 330 us,
+// 833 TF/s.  Longest expert first and neighbouring tiles on one XCD: both
+// gradients 1079 -> 651 us together with the rows kernel's persistent grid.
 template <bool THROUGH, int BM, int BN, int WM, int WN>
 __global__ void __launch_bounds__((DirectTile<BM, BN, WM, WN, float>::NT))
     k_expert_weights_direct(ExpertArgs a, int m_tiles, int n_tiles) {
@@ -1232,7 +1302,11 @@ void run_rows_direct(const ExpertArgs& a, int tile_rows, int per_cu, hipStream_t
 
 // The least tile height, a multiple of 16, at which the tiles of 256 columns
 // still take no more rounds of the grid than at height 256; an expert's last
-// tile is taken to be half full.
+// tile is taken to be half full.  Tiles of 192 rows or fewer have a kernel of
+// that many: forward of 64 experts 512 -> 512, 512 slots each, 45 us against 52
+// with 256 rows; 16 experts 1024 -> 1024, 1024 each: 51 and 61.  Where 128 rows
+// do, two workgroups of 128 x 128 share a CU: 8 experts 512 -> 1024, 512 slots
+// each: 15.2 us against 17.8 with 192 rows and 20.6 with 256.
 int tile_height(int64_t slots, int n_experts, int64_t n_tiles) {
     const int64_t part = n_experts / 2;
     const int64_t rounds = ((slots / 256 + part + 1) * n_tiles + kCus - 1) / kCus;
@@ -1286,7 +1360,9 @@ void run_few(const ExpertArgs& a, hipStream_t s) {
 //    for) and at most 128 x 128 weights: 1024 experts, 64 slots each, 64 -> 64: 15
 //    against 43, 128 -> 128: 29 against 45, 256 -> 256: 76 against 71; 256 slots
 //    each, 128 -> 128: 79 against 79.
-//  - else copied tiles where rows allow it, or staged ones.
+//  - 32 x 32 tiles for up to 32 columns: both gradients of 16 experts 32 -> 256,
+//    8192 slots each, float32: 164 against 230 with wider ones, bfloat16: 82 and 89.
+//  - else copied tiles where rows allow it, or staged ones (128 x 128).
 template <class T, bool GRAD>
 void pick_rows(const ExpertArgs& a, hipStream_t s) {
     const int64_t N = GRAD ? a.d_in : a.d_out, per = a.slots / a.n_experts;
@@ -1341,16 +1417,24 @@ bool wide_weight_tiles(int64_t slots, int n_experts, int d_in, int d_out) {
     return slots / n_experts >= 2048 && d_in > 128 && d_out > 128;
 }
 
+// Copied tiles where rows allow it, also of narrow weights (both gradients of 16
+// experts 32 -> 256, 8192 slots each, bfloat16: 50 us against 82 with 32 x 64
+// staged ones; 1024 experts 32 -> 64, 128 slots each: 37 and 44).  Staged ones are
+// 32 x 64 where a side has at most 64 (float32, 1024 experts, 128 slots each,
+// 63 -> 32: 90 against 145 with 128 x 128, 64 -> 64: 102 and 151; 16 experts
+// 64 -> 256, 8192 each: 235 and 241).
 template <class T>
 void pick_weights(const ExpertArgs& a, hipStream_t s) {
-    if (a.d_out <= 32 || a.d_in <= 32)
+    if (sizeof(T) == 2 && direct_weights(a)) {
+        if (wide_weight_tiles(a.slots, a.n_experts, a.d_in, a.d_out))
+            run_weights_direct<256, 256, 128, 64>(a, s);
+        else
+            run_weights_direct<128, 128, 64, 64>(a, s);
+    } else if (a.d_out <= 64 || a.d_in <= 64) {
         run_weights<T, 32, 64, 32, 64>(a, s);
-    else if (sizeof(T) == 4 || !direct_weights(a))
+    } else {
         run_weights<T, 128, 128, 64, 64>(a, s);
-    else if (wide_weight_tiles(a.slots, a.n_experts, a.d_in, a.d_out))
-        run_weights_direct<256, 256, 128, 64>(a, s);
-    else
-        run_weights_direct<128, 128, 64, 64>(a, s);
+    }
     if (a.chunk) {
         const int64_t per = (int64_t)a.d_out * a.d_in + (a.db ? a.d_out : 0);
         k_expert_sum<<<dim3((unsigned)((per + 255) / 256), a.n_experts), 256, 0, s>>>(a);

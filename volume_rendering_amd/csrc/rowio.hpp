@@ -26,6 +26,12 @@ struct RowIO {
         v.u = u32x4{0u, 0u, 0u, 0u};
         return v;
     }
+    // A whole piece from p on.
+    static __device__ __forceinline__ Vec load_whole(const T* p) {
+        Vec v;
+        v.u = reinterpret_cast<const Loose*>(p)->u;
+        return v;
+    }
     // Elements c .. c + PER - 1 of a row of `width` (those past it: zero).
     static __device__ __forceinline__ Vec load(const T* row, int64_t c, int64_t width) {
         Vec v = zero();
