@@ -177,3 +177,29 @@ def test_same_bits_and_another_stream():
             torch.cuda.synchronize()
         for o in outs[1:]:
             assert torch.equal(o[0], outs[0][0]) and torch.equal(o[1], outs[0][1])
+
+
+@pytest.mark.parametrize("V", [500, 9001, 70000])
+def test_loss_does_not_depend_on_a_shift(V):
+    """Logits around 1e4 and teacher logits around -2e4: the bound knows only
+    the differences within a row.  With R and Rt the largest of those, and
+    u = 2^-23: a student's logarithm is off by at most (2 R + chain + 2 R + 2) u
+    from the exponentials and their sum and 2 R u from its own difference, a
+    teacher's by (4 Rt + K + 8) u, and the K terms of p times a difference of two
+    logarithms (each at most R + Rt + ln V + ln K) add (K + 8) u of that."""
+    torch = torch_cuda()
+    import volume_rendering_amd as v
+    say(f"distill shifted logits V={V}")
+    g = np.random.default_rng([11, V])
+    n, K, T = 6, 12, 2.0
+    z = (1e4 + 3 * g.standard_normal((n, V))).astype(np.float32)
+    t = (-2e4 + 3 * g.standard_normal((n, K))).astype(np.float32)
+    ids = np.stack([g.permutation(V)[:K] for _ in range(n)]).astype(np.int32)
+    want, _, _ = R.distill(z.astype(np.float64), t.astype(np.float64), ids, T)
+    loss = torch.empty(n, device="cuda")
+    v.nerf_distill_topk(torch.from_numpy(z).cuda(), torch.from_numpy(t).cuda(), torch.from_numpy(ids).cuda(), T, loss)
+    rng_z, rng_t = (z.max(1) - z.min(1)).astype(np.float64) / T, (t.max(1) - t.min(1)).astype(np.float64) / T
+    chain = V / 64 + 24
+    tol = T * T * U * (6 * rng_z + chain + 4 * rng_t + K + 16
+                       + (K + 8) * (rng_z + rng_t + np.log(V) + np.log(K)))
+    assert np.all(np.abs(_f64(loss) - want) <= tol), (np.abs(_f64(loss) - want), tol)

@@ -202,6 +202,17 @@ def test_expert_layer_and_its_gradient(case, bf16, through_order):
     assert torch.equal(dx2, dx) and torch.equal(dw2, dw)
 
 
+NARROW = [(1, 3), (3, 1), (2, 9), (7, 5), (5, 70), (8, 67), (9, 40), (66, 3), (71, 8), (129, 135), (133, 66), (65, 129)]
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("d_in,d_out", NARROW)
+def test_widths_around_a_piece(d_in, d_out, bf16):
+    """Rows shorter than 16 bytes, and ones whose last piece is nearly empty or
+    nearly full, in groups long enough for the widest tiles."""
+    test_expert_layer_and_its_gradient((350, 2, 3, d_in, d_out, 0.1), bf16, True)
+
+
 def test_gradient_of_no_slots_is_zero():
     torch = torch_cuda()
     import volume_rendering_amd as v

@@ -1,4 +1,4 @@
-"""MI355X-native NeRF forward-render hot path.
+"""MI355X-native NeRF rendering and training, and routed many-network fields.
 
 The work runs in ``libnerf_mi355x.so`` (hand-written HIP for gfx950) behind
 the C ABI declared in ``include/nerf_mi355x.h``; this package is its thin
