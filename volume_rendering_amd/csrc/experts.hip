@@ -1356,22 +1356,30 @@ void run_few(const ExpertArgs& a, hipStream_t s) {
 //    against 12.
 //  - below 32: 32-slot tiles.  1024 experts 256 -> 256, 16 slots each: 42 against
 //    51 with copied tiles; 64 experts 512 -> 512, 32 each: 18 against 16.
+//  - also with at most 64 columns, of which the larger tiles leave half empty, and
+//    at most 512 k in bfloat16: 8 experts, 32768 slots each, 64 -> 64: 32 against 44
+//    (float32: 59 against 80), 512 -> 64: 97 against 97; 8192 each, 1024 -> 64: 61
+//    against 56 (float32: 163 against 233), 2047 -> 63: 142 against 130 (float32: 322
+//    against 463); 1024 experts, 256 each, 64 -> 64: 36 against 76; but with 128
+//    columns, 8 experts, 32768 each, 64 -> 128: 58 against 45 (float32: 111 against
+//    89).
 //  - also below 256 with more than 63 experts (whose tiles have to be searched
-//    for) and at most 128 x 128 weights: 1024 experts, 64 slots each, 64 -> 64: 15
-//    against 43, 128 -> 128: 29 against 45, 256 -> 256: 76 against 71; 256 slots
-//    each, 128 -> 128: 79 against 79.
+//    for) and at most 128 x 128 weights: 1024 experts, 64 slots each, 128 -> 128:
+//    29 against 45, 256 -> 256: 76 against 71; 256 slots each, 128 -> 128: 79
+//    against 79.
 //  - 32 x 32 tiles for up to 32 columns: both gradients of 16 experts 32 -> 256,
 //    8192 slots each, float32: 164 against 230 with wider ones, bfloat16: 82 and 89.
 //  - else copied tiles where rows allow it, or staged ones (128 x 128).
 template <class T, bool GRAD>
 void pick_rows(const ExpertArgs& a, hipStream_t s) {
-    const int64_t N = GRAD ? a.d_in : a.d_out, per = a.slots / a.n_experts;
+    const int64_t N = GRAD ? a.d_in : a.d_out, K = GRAD ? a.d_out : a.d_in, per = a.slots / a.n_experts;
+    const bool small = N <= 64 && (K <= 512 || sizeof(T) == 4);
     const bool narrow = a.n_experts > 63 && (int64_t)a.d_in * a.d_out <= 128 * 128;
     if (!GRAD && a.slots <= kFewSlots && per < 16)
         run_few<T>(a, s);
     else if (N <= 32)
         run_rows<T, GRAD, 32, 32, 32, 32>(a, s);
-    else if (per < (narrow ? 256 : 32))
+    else if (small || per < (narrow ? 256 : 32))
         run_rows<T, GRAD, 32, 64, 32, 64>(a, s);
     else if (sizeof(T) == 2 && direct_rows(a, GRAD))
         pick_rows_direct<GRAD>(a, s);
