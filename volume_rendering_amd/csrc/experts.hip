@@ -1368,7 +1368,7 @@ void run_few(const ExpertArgs& a, hipStream_t s) {
 //    29 against 45, 256 -> 256: 76 against 71; 256 slots each, 128 -> 128: 79
 //    against 79.
 //  - 32 x 32 tiles for up to 32 columns: both gradients of 16 experts 32 -> 256,
-//    8192 slots each, float32: 164 against 230 with wider ones, bfloat16: 82 and 89.
+//    8192 slots each, float32: 164 against 230 with wider ones, bfloat16: 7 less.
 //  - else copied tiles where rows allow it, or staged ones (128 x 128).
 template <class T, bool GRAD>
 void pick_rows(const ExpertArgs& a, hipStream_t s) {
