@@ -90,8 +90,11 @@ def distill(logits, t_logits, t_ids, temperature, row_scale=None):
         for r in range(n):
             z = logits[r] / T
             m = z.max()
-            lse[r] = m if np.isneginf(m) else m + np.log(np.exp(z - m).sum())
-            q = np.zeros(V) if np.isneginf(lse[r]) else np.exp(z - lse[r])
+            none = np.isneginf(m)
+            total = 0.0 if none else np.exp(z - m).sum()  # (kept apart from m, which may be too large to add it to)
+            lse[r] = m if none else m + np.log(total)
+            logq = np.full(V, -np.inf) if none else (z - m) - np.log(total)
+            q = np.zeros(V) if none else np.exp(z - m) / total
             ok = (t_ids[r] >= 0) & (t_ids[r] < V)
             t, idx = t_logits[r][ok] / T, t_ids[r][ok]
             if t.size == 0 or np.isneginf(t.max()):
@@ -100,7 +103,7 @@ def distill(logits, t_logits, t_ids, temperature, row_scale=None):
             p = np.exp(logp)
             for pj, lp, v in zip(p, logp, idx):
                 if pj != 0:  # (a NaN counts)
-                    loss[r] += pj * (lp - (-np.inf if np.isneginf(lse[r]) else z[v] - lse[r]))
+                    loss[r] += pj * (lp - logq[v])
             loss[r] *= T * T
             g = q * p.sum()
             np.subtract.at(g, idx, p)
