@@ -617,7 +617,10 @@ nerf_status nerf_distill_topk(const void* logits, int dtype, int64_t ld_logits, 
                               const float* row_scale, float* loss, float* lse, void* grad, int64_t ld_grad,
                               void* workspace, size_t workspace_bytes, void* stream);
 
-/* The gradient alone, from the lse that nerf_distill_topk returned. */
+/* The gradient alone, from the lse that nerf_distill_topk returned for the same
+ * logits and temperature: q = exp(logits / T - lse), to |lse| 2^-23 of q.  For
+ * |lse| >= 64 (logits far from zero, or all masked), where that would be more
+ * than 2^-17, the row's maximum and sum are computed again and lse is not used. */
 nerf_status nerf_distill_topk_grad(const void* logits, int dtype, int64_t ld_logits, int64_t n, int64_t classes,
                                    const float* t_logits, const int32_t* t_ids, int top, float temperature,
                                    const float* row_scale, const float* lse, void* grad, int64_t ld_grad,

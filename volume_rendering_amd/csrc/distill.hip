@@ -334,19 +334,40 @@ __global__ void __launch_bounds__(kSplitThreads) k_distill_join(DistillArgs a, i
                                  all.s == 0.0f ? 0.0f : 1.0f / all.s, scale);
 }
 
-// Gradient from a saved log-sum-exp: q = e^(z - lse).
+// Gradient from a saved log-sum-exp: q = e^(z - lse).  Rounding lse, one float32
+// of the size of the largest z, and its product with T is a relative error of up
+// to |lse| 2^-23 of q: 2^-17 for the |lse| < 64 of logits a softmax is meant for.
+// A row beyond (shifted, or all masked with the type's lowest value, where ln of
+// the sum is lost beside the maximum, or lse not finite) is done whole by one of
+// its workgroups (in turn, so that all XCDs have some), which finds the maximum
+// and the sum again: the same error as with the loss, for one more read of the row
+// (8192 x 4096 bfloat16: 41 us if all rows are such, 28 if none; 4096 x 128000:
+// 1027 and 394).
+constexpr float kLseLargest = 64.0f;
+
 template <class T>
 __global__ void __launch_bounds__(kSplitThreads) k_distill_grad(DistillArgs a, int gsplits) {
+    __shared__ MaxSum scratch[kSplitThreads / 64];
     __shared__ TopLds top;
     const int64_t r = blockIdx.x / gsplits;
     const int i = blockIdx.x % gsplits, lane = threadIdx.x & 63;
+    const T* row = (const T*)a.logits + r * a.ld;
+    const float c = kLog2e / a.temperature, lse = a.lse[r];
     if (threadIdx.x < 64) keep_top<T>(top, teacher_row(a, r, lane), a.top, lane);
-    __syncthreads();
     int64_t c0, c1;
     split_range(a.classes, gsplits, i, c0, c1);
+    __syncthreads();
+    float m = lse * a.temperature, inv = 1.0f;
+    if (!(fabsf(lse) < kLseLargest)) {  // (the same for all of a row's workgroups)
+        if (i != r % gsplits) return;
+        c0 = 0;
+        c1 = a.classes;
+        const MaxSum v = scan_row<T, kSplitThreads>(row, 0, c1, c, scratch);
+        m = v.m;
+        inv = v.s == 0.0f ? 0.0f : 1.0f / v.s;
+    }
     const float scale = a.temperature * (a.row_scale ? a.row_scale[r] : 1.0f);
-    write_grad<T, kSplitThreads>(a, top, (const T*)a.logits + r * a.ld, (T*)a.grad + r * a.ld_grad, c0, c1,
-                                 kLog2e / a.temperature, shift_of(a.lse[r] * a.temperature), 1.0f, scale);
+    write_grad<T, kSplitThreads>(a, top, row, (T*)a.grad + r * a.ld_grad, c0, c1, c, shift_of(m), inv, scale);
 }
 
 // Workgroups per row of a gradient sweep: ranges of 16384 classes (64 x 128000
