@@ -94,3 +94,71 @@ def test_gradients_of_rows_of_the_lowest_value(V, T, bf16):
     t, ids = g.standard_normal((n, K)), np.stack([g.permutation(V)[:K] for _ in range(n)])
     hx, ht, _, _, *grads = _run(z, t, ids, T, bf16)
     _check_gradient(hx, ht, ids, T, bf16, None, grads)
+
+
+def _loss_tolerance(hx, ht, ids, T):
+    """loss = T sum p (T (ln p + ln sum) - (s - max)): an entry's p is off by (4 min(Rt,
+    120) + 2 K + 8) u of itself (below e^-120 it is nothing), the logarithm of the sum
+    by the sum's relative error, the rest by 8 u of the terms."""
+    n, V = hx.shape
+    K = ids.shape[1]
+    m = hx.max(1, keepdims=True)
+    d = (hx - m) / T
+    spread = np.where(d > -120, -d, 0).max(1, keepdims=True)
+    t = (ht - ht.max(1, keepdims=True)) / T
+    p = np.exp(t)
+    p /= p.sum(1, keepdims=True)
+    logp = np.where(p > 0, np.log(np.where(p > 0, p, 1)), 0)
+    logs = np.log(np.exp(d).sum(1, keepdims=True))
+    size = np.take_along_axis(m - hx, ids, 1) + T * (np.abs(logp) + logs)
+    rel = 4 * np.minimum(-t.min(1, keepdims=True), 120) + 2 * K + 16
+    return T * U * (p * (size * rel + T * (2 * (1.5 * spread + 2) + V / 64 + 24))).sum(1) + 1e-44
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("T", [0.25, 0.5, 1.0, 2.0])
+@pytest.mark.parametrize("V", [70, 6000, 40001])
+def test_teacher_mass_on_a_class_of_the_lowest_value(V, T, bf16):
+    """The loss of such a class is p T 3.4e38, which is finite."""
+    say(f"distill mass on the lowest V={V} T={T} bf16={bf16}")
+    g = np.random.default_rng([23, V])
+    n, K = 4, 8
+    z, t = 2 * g.standard_normal((n, V)), g.standard_normal((n, K))
+    ids = np.stack([g.permutation(V)[:K] for _ in range(n)])
+    z[np.arange(n), ids[:, 3]] = LOWEST[bf16]
+    t[:, 3] -= 3.0 * T  # (its p is a few hundredths)
+    hx, ht, loss, _, *_ = _run(z, t, ids, T, bf16)
+    want, _, _ = R.distill(hx, ht, ids, T)
+    assert np.all(np.abs(loss - want) <= _loss_tolerance(hx, ht, ids, T)), (loss, want)
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("T", [1e-45, 1e-40, 1e-30, 1e-10, 1e4, 1e37, 3e38])
+@pytest.mark.parametrize("V", [70, 9000])
+def test_temperatures_far_from_one(V, T, bf16):
+    """Down to the smallest positive one both distributions are single classes; at
+    the largest they are even, and the loss may pass the type's range."""
+    say(f"distill T={T} V={V} bf16={bf16}")
+    T = float(np.float32(T))
+    g = np.random.default_rng([24, V])
+    n, K = 4, 7
+    z, t = 2 * g.standard_normal((n, V)), g.standard_normal((n, K)).astype(np.float32).astype(np.float64)
+    ids = np.stack([g.permutation(V)[:K] for _ in range(n)])
+    z[0, :9] = 30.0  # equal largest classes
+    hx, ht, loss, _, both, alone = _run(z, t, ids, T, bf16)
+    want, _, grad = R.distill(hx, ht, ids, T)
+    inside = want < 3e38
+    assert np.all(np.abs(loss - want)[inside] <= _loss_tolerance(hx, ht, ids, T)[inside]), (loss, want)
+    assert np.all(loss[~inside] >= 3e38)
+    d = (hx - hx.max(1, keepdims=True)) / T
+    q = np.exp(d)
+    q /= q.sum(1, keepdims=True)
+    p = np.abs(q - grad / T)
+    # (exponents above -120 count; a temperature below 2^-126 is itself rounded to few bits in 1 / T)
+    spread = np.where(d > -120, -d, 0).max(1, keepdims=True)
+    rt = np.minimum((ht.max(1) - ht.min(1))[:, None] / T, 120)
+    tol = T * U * (q * (2 * (1.5 * spread + 2) + V / 64 + 24 + 64 + 8) + (p + q) * (4 * rt + 2 * K + 8)) + 1e-37
+    if bf16:
+        tol += 2.0 ** -8 * np.abs(grad)
+    for got in (both, alone):
+        assert np.all(np.abs(got - grad) <= tol)

@@ -11,6 +11,7 @@
 // the exponent's error relative to s - m, however large the logits are.
 #include <hip/hip_runtime.h>
 
+#include <cfloat>
 #include <cmath>
 
 #include "common.hpp"
@@ -28,6 +29,10 @@ constexpr float kLog2e = 1.44269504088896341f;
 struct MaxSum {
     float m, s;
 };
+
+// 1 / T and log2(e) / T, kept finite for the T (below 2^-127) that have none: a
+// difference of logits above 2^-120 is then still past the range of an exponential.
+__device__ __forceinline__ float over_t(float x, float temperature) { return fminf(x / temperature, FLT_MAX); }
 
 // What to subtract for the maximum m: with m = -inf every logit is -inf (or NaN)
 // and 2^((x - 0) c) is 0 (or NaN), as it has to be.
@@ -118,7 +123,7 @@ struct Teacher {
 __device__ __forceinline__ Teacher teacher_row(const DistillArgs& a, int64_t row, int lane) {
     Teacher t;
     float z[kTopPerLane], m = -INFINITY, nan = 0.0f;
-    const float inv_t = 1.0f / a.temperature;
+    const float inv_t = over_t(1.0f, a.temperature);
 #pragma unroll
     for (int u = 0; u < kTopPerLane; ++u) {
         const int j = lane + 64 * u;
@@ -151,8 +156,10 @@ __device__ __forceinline__ Teacher teacher_row(const DistillArgs& a, int64_t row
     return t;
 }
 
-// Loss of a row from its maximum and sum, by one wave; ln q_v = (s_v - m) / T - ln sum,
-// which stays accurate however large the logits are.
+// Loss of a row from its maximum and sum, by one wave.  With ln q_v = (s_v - m) / T - ln sum,
+//   loss = T sum_j p_j (T (ln p_j + ln sum) - (s_{i_j} - m)),
+// which stays accurate however large the logits are, and in range where (s - m) / T
+// or T^2 is not (a class of the type's lowest value, a temperature far from one).
 template <class T>
 __device__ __forceinline__ float row_loss(const DistillArgs& a, const Teacher& t, const T* row, const MaxSum& v) {
     float sum = 0.0f;
@@ -160,11 +167,11 @@ __device__ __forceinline__ float row_loss(const DistillArgs& a, const Teacher& t
 #pragma unroll
     for (int u = 0; u < kTopPerLane; ++u)
         if (t.id[u] >= 0 && t.p[u] != 0.0f) {
-            const float logq = v.m == -INFINITY ? (v.s == 0.0f ? -INFINITY : v.s)
-                                                : ((float)row[t.id[u]] - v.m) / a.temperature - log_s;
-            sum += t.p[u] * (t.logp[u] - logq);
+            const float below = v.m == -INFINITY ? (v.s == 0.0f ? INFINITY : v.s)  // (no student, or NaN)
+                                                 : a.temperature * (t.logp[u] + log_s) - ((float)row[t.id[u]] - v.m);
+            sum += t.p[u] * below;
         }
-    return a.temperature * a.temperature * wave_sum(sum);
+    return a.temperature * wave_sum(sum);
 }
 
 // The gradient at the teacher's classes: after the sweep over the row has
@@ -247,7 +254,7 @@ __global__ void __launch_bounds__(NT) k_distill_rows(DistillArgs a) {
     __shared__ TopLds top;
     const int64_t r = blockIdx.x;
     const T* row = (const T*)a.logits + r * a.ld;
-    const float c = kLog2e / a.temperature;
+    const float c = over_t(kLog2e, a.temperature);
     const int lane = threadIdx.x & 63;
     const MaxSum v = scan_row<T, NT>(row, 0, a.classes, c, scratch);
     if (threadIdx.x < 64) {
@@ -288,7 +295,7 @@ __global__ void __launch_bounds__(kSplitThreads) k_distill_part(DistillArgs a, i
     const int i = blockIdx.x % splits;
     int64_t c0, c1;
     split_range(a.classes, splits, i, c0, c1);
-    const MaxSum v = scan_row<T, kSplitThreads>((const T*)a.logits + r * a.ld, c0, c1, kLog2e / a.temperature, scratch);
+    const MaxSum v = scan_row<T, kSplitThreads>((const T*)a.logits + r * a.ld, c0, c1, over_t(kLog2e, a.temperature), scratch);
     if (threadIdx.x == 0) {
         a.part[2 * (r * splits + i)] = v.m;
         a.part[2 * (r * splits + i) + 1] = v.s;
@@ -299,9 +306,9 @@ __device__ __forceinline__ MaxSum joined_parts(const DistillArgs& a, int64_t r, 
     MaxSum v{-INFINITY, 0.0f};
     for (int i = lane; i < splits; i += 64) {
         const MaxSum o{a.part[2 * (r * splits + i)], a.part[2 * (r * splits + i) + 1]};
-        v = join(v, o, kLog2e / a.temperature);
+        v = join(v, o, over_t(kLog2e, a.temperature));
     }
-    return block_join<64>(v, kLog2e / a.temperature, nullptr);
+    return block_join<64>(v, over_t(kLog2e, a.temperature), nullptr);
 }
 
 // grid: [n][max(gsplits, 1)]; the first workgroup of a row writes its loss.
@@ -330,7 +337,7 @@ __global__ void __launch_bounds__(kSplitThreads) k_distill_join(DistillArgs a, i
     int64_t c0, c1;
     split_range(a.classes, gsplits, i, c0, c1);
     const float scale = a.temperature * (a.row_scale ? a.row_scale[r] : 1.0f);
-    write_grad<T, kSplitThreads>(a, top, row, (T*)a.grad + r * a.ld_grad, c0, c1, kLog2e / a.temperature, shift_of(all.m),
+    write_grad<T, kSplitThreads>(a, top, row, (T*)a.grad + r * a.ld_grad, c0, c1, over_t(kLog2e, a.temperature), shift_of(all.m),
                                  all.s == 0.0f ? 0.0f : 1.0f / all.s, scale);
 }
 
@@ -352,13 +359,13 @@ __global__ void __launch_bounds__(kSplitThreads) k_distill_grad(DistillArgs a, i
     const int64_t r = blockIdx.x / gsplits;
     const int i = blockIdx.x % gsplits, lane = threadIdx.x & 63;
     const T* row = (const T*)a.logits + r * a.ld;
-    const float c = kLog2e / a.temperature, lse = a.lse[r];
+    const float c = over_t(kLog2e, a.temperature), lse = a.lse[r];
     if (threadIdx.x < 64) keep_top<T>(top, teacher_row(a, r, lane), a.top, lane);
     int64_t c0, c1;
     split_range(a.classes, gsplits, i, c0, c1);
     __syncthreads();
     float m = lse * a.temperature, inv = 1.0f;
-    if (!(fabsf(lse) < kLseLargest)) {  // (the same for all of a row's workgroups)
+    if (!(fabsf(lse) < kLseLargest && fabsf(m) < INFINITY)) {  // (the same for all of a row's workgroups)
         if (i != r % gsplits) return;
         c0 = 0;
         c1 = a.classes;
