@@ -385,7 +385,14 @@ def _matrix(t, what: str):
 
 
 def _ws(workspace):
-    return (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    """Device pointer and bytes of a workspace ((0, 0) for None)."""
+    if workspace is None:
+        return 0, 0
+    if not workspace.is_contiguous():
+        raise NerfError("workspace: tensor must be contiguous")
+    if not workspace.is_cuda:
+        raise NerfError("workspace: not a device tensor")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def nerf_route_workspace_size(n: int, k: int, n_experts: int) -> int:
