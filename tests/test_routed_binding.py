@@ -32,3 +32,18 @@ def test_workspaces_are_contiguous_device_tensors(ws, why):
 
 def test_no_workspace_is_a_workspace():
     assert B._ws(None) == (0, 0)
+
+
+def test_gradient_of_a_layer_needs_x_or_weight():
+    z = torch.zeros
+    with pytest.raises(v.NerfError, match="x and weight"):
+        v.nerf_expert_linear_grad(z(8, 5), None, None, z(4, dtype=I32), z(8, 7))
+    # one of them is enough to name the shapes: what is refused next is the host tensor
+    with pytest.raises(v.NerfError, match="dz: not a device tensor"):
+        v.nerf_expert_linear_grad(z(8, 5), None, z(3, 5, 7), z(4, dtype=I32), z(8, 7))
+    with pytest.raises(v.NerfError, match="dz: not a device tensor"):
+        v.nerf_expert_linear_grad(z(8, 5), z(8, 7), None, z(4, dtype=I32), None, z(3, 5, 7))
+    with pytest.raises(v.NerfError, match="weight: 2 dimensions"):
+        v.nerf_expert_linear_grad(z(8, 5), None, z(5, 7), z(4, dtype=I32), z(8, 7))
+    with pytest.raises(v.NerfError, match="x: "):
+        v.nerf_expert_linear_grad(z(8, 5), z(8, 6), z(3, 5, 7), z(4, dtype=I32), z(8, 7))

@@ -457,14 +457,22 @@ def nerf_route_combine_grad(dout, y, offsets, place, weights, dy, dweights=None)
            "nerf_route_combine_grad")
 
 
-def _expert_layer(x, weight, ld_y, order, k, relu):
-    if weight.dim() != 3:
-        raise NerfError(f"weight: {weight.dim()} dimensions, expected 3")
-    E, d_out, d_in = weight.shape
-    if x.dim() != 2 or x.shape[1] != d_in:
+def _expert_layer(x, weight, d_out, offsets, ld_y, order, k, relu):
+    """The layer of ``x`` and ``weight``, of which one may be None, and its
+    experts and widths."""
+    if weight is not None:
+        if weight.dim() != 3:
+            raise NerfError(f"weight: {weight.dim()} dimensions, expected 3")
+        E, d_out, d_in = weight.shape
+    elif x is not None:
+        E, d_in = offsets.numel() - 1, _matrix(x, "x")[1]
+    else:
+        raise NerfError("x and weight: both are None")
+    if x is not None and (x.dim() != 2 or x.shape[1] != d_in):
         raise NerfError(f"x: shape {tuple(x.shape)}, expected [rows, {d_in}]")
-    return nerf_expert_layer(_dtype_of(weight, "weight"), E, d_in, d_out, int(relu), k if order is not None else 0,
-                             x.shape[0], _ld(x), ld_y)
+    dtype = _dtype_of(x, "x") if weight is None else _dtype_of(weight, "weight")
+    return nerf_expert_layer(dtype, E, d_in, d_out, int(relu), k if order is not None else 0,
+                             0 if x is None else x.shape[0], _ld(x), ld_y), E, d_out, d_in
 
 
 def nerf_expert_linear(x, weight, bias, offsets, y, order=None, k=1, relu=False):
@@ -473,8 +481,7 @@ def nerf_expert_linear(x, weight, bias, offsets, y, order=None, k=1, relu=False)
     [slots, d_in], or the samples' [n, d_in] rows with the plan's ``order`` and
     ``k``.  Rows of ``x`` and ``y`` may be strided."""
     torch = _torch()
-    L = _expert_layer(x, weight, _ld(y), order, k, relu)
-    E, d_out, d_in = weight.shape
+    L, E, d_out, d_in = _expert_layer(x, weight, None, offsets, _ld(y), order, k, relu)
     slots, i32, dt = _matrix(y, "y")[0], torch.int32, weight.dtype
     _check(lib().nerf_expert_linear(C.byref(L), _tensor(x, "x", dt, x.shape, True),
                                     _tensor(weight, "weight", dt, weight.shape),
@@ -494,19 +501,23 @@ def nerf_expert_linear_grad(dz, x, weight, offsets, dx=None, dweight=None, dbias
     """Gradients of nerf_expert_linear from ``dz`` [slots, d_out] (at the value
     before its activation): ``dx`` [slots, d_in] (zero where x <= 0 with
     ``relu_x``), float32 ``dweight`` [E, d_out, d_in] and ``dbias`` [E, d_out],
-    each optional."""
+    each optional.  ``x`` may be None without ``dweight`` and ``relu_x`` (and
+    ``order``, which names its rows, then does nothing), ``weight`` without
+    ``dx``."""
     torch = _torch()
-    L = _expert_layer(x, weight, _ld(dz), order, k, relu_x)
-    E, d_out, d_in = weight.shape
-    slots, i32, dt, f32 = _matrix(dz, "dz")[0], torch.int32, weight.dtype, torch.float32
+    slots, d_out = _matrix(dz, "dz")
+    if x is None:
+        order = None
+    L, E, d_out, d_in = _expert_layer(x, weight, d_out, offsets, _ld(dz), order, k, relu_x)
+    i32, dt, f32 = torch.int32, (x if weight is None else weight).dtype, torch.float32
     ws, wsb = _ws(workspace)
     _check(lib().nerf_expert_linear_grad(C.byref(L), _tensor(dz, "dz", dt, (slots, d_out), True),
-                                         _tensor(x, "x", dt, x.shape, True),
-                                         _tensor(weight, "weight", dt, weight.shape),
+                                         _tensor(x, "x", dt, x is not None and x.shape, True),
+                                         _tensor(weight, "weight", dt, (E, d_out, d_in)),
                                          _tensor(offsets, "offsets", i32, (E + 1,)),
                                          _tensor(order, "order", i32, (slots,)), slots,
                                          _tensor(dx, "dx", dt, (slots, d_in)),
-                                         _tensor(dweight, "dweight", f32, weight.shape),
+                                         _tensor(dweight, "dweight", f32, (E, d_out, d_in)),
                                          _tensor(dbias, "dbias", f32, (E, d_out)), ws, wsb, _stream_handle()),
            "nerf_expert_linear_grad")
 
