@@ -557,7 +557,8 @@ typedef struct {
  * [n_experts, d_out, d_in]; bias: device float32 [n_experts, d_out] or NULL;
  * offsets, order: from nerf_route_plan, order NULL if x is in slot order;
  * y: device [slots, d_out].  Errors: null pointers, bad dtype, sizes, strides
- * or alignment, x_rows < slots without order. */
+ * or alignment, x_rows < slots without order; NERF_ERR_UNSUPPORTED for more
+ * than 4096 experts, and for slots x columns beyond 2^38 or slots near 2^31. */
 nerf_status nerf_expert_linear(const nerf_expert_layer* layer, const void* x, const void* weights, const float* bias,
                                const int32_t* offsets, const int32_t* order, int64_t slots, void* y, void* stream);
 

@@ -1,5 +1,6 @@
 // Host-side checks of what the routed-field entry points hand to the launchers,
-// without a GPU: the exact quotient that turns pairs into samples.  The real argument checks (experts_abi.cpp) with stand-ins for the
+// without a GPU: the exact quotient that turns pairs into samples, and how large
+// calls may be.  The real argument checks (experts_abi.cpp) with stand-ins for the
 // launchers and HIP calls; nothing is dereferenced.
 #include <hip/hip_runtime.h>
 
@@ -63,6 +64,11 @@ static nerf_status forward(int dtype, int64_t slots, int experts, int d_in, int 
     nerf_expert_layer L{dtype, experts, d_in, d_out, 0, k, slots, 0, 0};
     return nerf_expert_linear(&L, F, F, F, I, order, slots, F, nullptr);
 }
+static nerf_status backward(int dtype, int64_t slots, int experts, int d_in, int d_out) {
+    nerf_expert_layer L{dtype, experts, d_in, d_out, 0, 1, slots, 0, 0};
+    return nerf_expert_linear_grad(&L, F, F, F, I, nullptr, slots, F, F, F, nullptr, 0, nullptr);
+}
+
 int main() {
     // pair / k by multiplication: exact for each k at and around its multiples, to the last pair
     for (int64_t k = 1; k <= NERF_MAX_CHOICES; ++k) {
@@ -82,6 +88,22 @@ int main() {
     CHECK(forward(NERF_BF16, 10, 4, 16, 24, 7, nullptr) == NERF_OK);  // without an order a slot is its own row
     for (int64_t p : {(int64_t)0, (int64_t)1, (int64_t)7, ((int64_t)1 << 31) - 1})
         CHECK((int64_t)(((uint64_t)p * g_args.k_mul) >> g_args.k_shift) == p);
+
+    // sizes that fit the card: none is refused
+    int n = 0;
+    for (int dt : {NERF_F32, NERF_BF16})
+        for (int64_t slots : {(int64_t)1 << 20, (int64_t)1 << 22, (int64_t)5000000, (int64_t)1 << 24, (int64_t)1 << 27, (int64_t)1 << 30})
+            for (int d : {1, 8, 32, 64, 65, 256, 1024, 4096, 16384, 65536})
+                for (int e : {1, 64, 4096}) {
+                    const double bytes = (double)(slots * (8 + d)) * (dt == NERF_F32 ? 4 : 2);
+                    if (bytes > 250e9) continue;
+                    CHECK(forward(dt, slots, e, 8, d, 1, nullptr) == NERF_OK);
+                    CHECK(forward(dt, slots, e, d, 8, 1, nullptr) == NERF_OK);
+                    if ((double)e * d * 8 * 4 < 20e9) CHECK(backward(dt, slots, e, d, 8) == NERF_OK);
+                    ++n;
+                }
+    CHECK(n > 150);
+    CHECK(forward(NERF_BF16, ((int64_t)1 << 31) - 1, 1, 8, 8, 1, nullptr) == NERF_ERR_UNSUPPORTED);
     std::printf("all %ld checks passed\n", g_checks);
     return 0;
 }

@@ -1,5 +1,5 @@
 """What the routed-field calls hand to their launchers (no GPU): the pairs'
-quotient for every number of choices.
+quotient for every number of choices, and no refusal of sizes that fit the card.
 ``tests/native/host_expert_limits.cpp`` with ``csrc/experts_abi.cpp``."""
 import os
 import shutil

@@ -105,10 +105,12 @@ nerf_status check_layer(const char* who, const nerf_expert_layer* L, const int32
                  NERF_MAX_CHOICES);
     if (L->n_experts > NERF_MAX_EXPERTS)
         return nerf_fail(NERF_ERR_UNSUPPORTED, "%s: n_experts %d above %d", who, L->n_experts, NERF_MAX_EXPERTS);
-    // the smallest tiles: at most 256 work items per 32 slots x 32 columns
+    // The largest grids: four waves for each 128 slots x 128 columns, or, with up to
+    // 64 columns, a wave for each 32 slots.  (Tiles of 32 slots x 64 of more columns
+    // are for fewer than 2^20 slots, and few enough for any width.  Steps of 64 slots
+    // are counted in 32 bits, two past the end.)
     const int64_t width = L->d_in > L->d_out ? L->d_in : L->d_out;
-    // (and k-steps of 64 slots are counted in 32 bits, two past the end)
-    if (slots > kMaxPairs - 255 || (slots / 32 + L->n_experts + 1) * ((width + 31) / 32) * 256 > kMaxItems)
+    if (slots > kMaxPairs - 255 || (slots / 128 + L->n_experts + 1) * ((width + 127) / 128) * 256 > kMaxItems)
         return nerf_fail(NERF_ERR_UNSUPPORTED, "%s: %lld slots x %lld columns exceed one launch", who,
                          (long long)slots, (long long)width);
     return NERF_OK;
