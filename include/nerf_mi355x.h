@@ -612,7 +612,7 @@ size_t nerf_distill_workspace_size(int64_t n, int64_t classes);
  * call (it must not overlap logits).  workspace: device, 16-byte aligned, or
  * NULL (allocated stream-ordered if needed).  Errors: null pointers, bad dtype,
  * sizes, strides or alignment, temperature not positive and finite, grad ==
- * logits, workspace too small. */
+ * logits, workspace too small; NERF_ERR_UNSUPPORTED for more than 2^40 logits. */
 nerf_status nerf_distill_topk(const void* logits, int dtype, int64_t ld_logits, int64_t n, int64_t classes,
                               const float* t_logits, const int32_t* t_ids, int top, float temperature,
                               const float* row_scale, float* loss, float* lse, void* grad, int64_t ld_grad,

@@ -104,6 +104,17 @@ int main() {
                 }
     CHECK(n > 150);
     CHECK(forward(NERF_BF16, ((int64_t)1 << 31) - 1, 1, 8, 8, 1, nullptr) == NERF_ERR_UNSUPPORTED);
+    // logits of many short rows and of few long ones
+    for (int64_t rows : {(int64_t)1, (int64_t)1 << 20, (int64_t)16777216, (int64_t)100000000, (int64_t)1 << 32})
+        for (int64_t classes : {(int64_t)1, (int64_t)10, (int64_t)1000, (int64_t)128000, ((int64_t)1 << 31) - 1}) {
+            if ((double)rows * (double)classes * 2 > 250e9) continue;
+            CHECK(nerf_distill_topk(F, NERF_BF16, 0, rows, classes, F, I, 1, 1.0f, nullptr, F, F, nullptr, 0, F, SIZE_MAX,
+                                    nullptr) == NERF_OK);
+            CHECK(nerf_distill_topk_grad(F, NERF_BF16, 0, rows, classes, F, I, 1, 1.0f, nullptr, F, F + 4, 0, nullptr) ==
+                  NERF_OK);
+        }
+    CHECK(nerf_distill_topk_grad(F, NERF_BF16, 0, (int64_t)1 << 30, 4096, F, I, 1, 1.0f, nullptr, F, F + 4, 0, nullptr) ==
+          NERF_ERR_UNSUPPORTED);
     std::printf("all %ld checks passed\n", g_checks);
     return 0;
 }

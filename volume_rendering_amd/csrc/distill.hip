@@ -382,6 +382,32 @@ __global__ void __launch_bounds__(kSplitThreads) k_distill_grad(DistillArgs a, i
 // 4096: 9.8 and 391).  Bound by memory: 5.4 TB/s.
 int grad_splits(int64_t classes) { return (int)((classes + 16383) / 16384); }
 
+// Rows r0 .. r0 + n - 1 of a call.
+template <class T>
+DistillArgs rows_from(DistillArgs a, int64_t r0, int64_t n) {
+    a.logits = (const T*)a.logits + r0 * a.ld;
+    a.n = n;
+    a.t_logits += r0 * a.top;
+    a.t_ids += r0 * a.top;
+    if (a.row_scale) a.row_scale += r0;
+    if (a.loss) a.loss += r0;
+    if (a.lse) a.lse += r0;
+    if (a.grad) a.grad = (T*)a.grad + r0 * a.ld_grad;
+    return a;
+}
+
+// A launch for as many rows of `items` work items each as it holds.
+template <class T, class F>
+void by_launches(const DistillArgs& a, int64_t items, F&& launch) {
+    const int64_t most = kMaxWorkItems / items;
+    for (int64_t r = 0; r < a.n; r += most) launch(rows_from<T>(a, r, a.n - r < most ? a.n - r : most));
+}
+
+template <class T, int NT>
+void run_rows(const DistillArgs& all, hipStream_t s) {
+    by_launches<T>(all, NT, [&](const DistillArgs& a) { k_distill_rows<T, NT><<<(unsigned)a.n, NT, 0, s>>>(a); });
+}
+
 // Threads by the length of a row, so that the rows in flight on the card stay
 // few enough to be cached between the sweeps, and short ones keep no idle waves.
 // Loss and gradient of bfloat16 rows, us:
@@ -391,17 +417,25 @@ int grad_splits(int64_t classes) { return (int)((classes + 16383) / 16384); }
 template <class T>
 void run_distill(const DistillArgs& a, hipStream_t s) {
     const int splits = distill_splits(a.n, a.classes);
-    if (splits > 1) {
+    if (splits > 1) {  // (fewer than 256 rows, and about 1024 workgroups)
         k_distill_part<T><<<(unsigned)(a.n * splits), kSplitThreads, 0, s>>>(a, splits);
         const int gs = a.grad ? splits : 1;
         k_distill_join<T><<<(unsigned)(a.n * gs), kSplitThreads, 0, s>>>(a, splits, gs);
     } else if (a.classes <= 4096) {
-        k_distill_rows<T, 64><<<(unsigned)a.n, 64, 0, s>>>(a);
+        run_rows<T, 64>(a, s);
     } else if (a.classes * sizeof(T) <= 65536) {
-        k_distill_rows<T, 256><<<(unsigned)a.n, 256, 0, s>>>(a);
+        run_rows<T, 256>(a, s);
     } else {
-        k_distill_rows<T, 1024><<<(unsigned)a.n, 1024, 0, s>>>(a);
+        run_rows<T, 1024>(a, s);
     }
+}
+
+template <class T>
+void run_grad(const DistillArgs& all, hipStream_t s) {
+    const int gs = grad_splits(all.classes);
+    by_launches<T>(all, (int64_t)gs * kSplitThreads, [&](const DistillArgs& a) {
+        k_distill_grad<T><<<(unsigned)(a.n * gs), kSplitThreads, 0, s>>>(a, gs);
+    });
 }
 
 }  // namespace
@@ -424,11 +458,10 @@ void launch_distill(bool bf16, const DistillArgs& a, hipStream_t s) {
 }
 
 void launch_distill_grad(bool bf16, const DistillArgs& a, hipStream_t s) {
-    const int gs = grad_splits(a.classes);
     if (bf16)
-        k_distill_grad<__bf16><<<(unsigned)(a.n * gs), kSplitThreads, 0, s>>>(a, gs);
+        run_grad<__bf16>(a, s);
     else
-        k_distill_grad<float><<<(unsigned)(a.n * gs), kSplitThreads, 0, s>>>(a, gs);
+        run_grad<float>(a, s);
 }
 
 }  // namespace nerf

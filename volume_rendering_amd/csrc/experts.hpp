@@ -11,6 +11,9 @@
 
 namespace nerf {
 
+// HIP launches hold fewer than 2^32 work items.
+constexpr int64_t kMaxWorkItems = ((int64_t)1 << 32) - 1;
+
 // Bits of the checked build (continuing CheckBit in common.hpp).
 enum ExpertCheckBit : unsigned {
     kCheckRouteSlot = 9,    // slot of a pair outside the slots, or a sorted pair outside the pairs

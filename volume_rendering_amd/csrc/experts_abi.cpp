@@ -15,8 +15,7 @@ namespace {
 
 constexpr int kMaxWidth = 65536;
 constexpr int64_t kMaxPairs = ((int64_t)1 << 31) - 1;
-// HIP launches hold fewer than 2^32 work items
-constexpr int64_t kMaxItems = ((int64_t)1 << 32) - 1;
+constexpr int64_t kMaxLogits = (int64_t)1 << 40;  // more than a card holds
 
 hipStream_t as_stream(void* s) { return reinterpret_cast<hipStream_t>(s); }
 bool aligned(const void* p, int bytes) { return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(bytes - 1)) == 0; }
@@ -110,7 +109,7 @@ nerf_status check_layer(const char* who, const nerf_expert_layer* L, const int32
     // are for fewer than 2^20 slots, and few enough for any width.  Steps of 64 slots
     // are counted in 32 bits, two past the end.)
     const int64_t width = L->d_in > L->d_out ? L->d_in : L->d_out;
-    if (slots > kMaxPairs - 255 || (slots / 128 + L->n_experts + 1) * ((width + 127) / 128) * 256 > kMaxItems)
+    if (slots > kMaxPairs - 255 || (slots / 128 + L->n_experts + 1) * ((width + 127) / 128) * 256 > kMaxWorkItems)
         return nerf_fail(NERF_ERR_UNSUPPORTED, "%s: %lld slots x %lld columns exceed one launch", who,
                          (long long)slots, (long long)width);
     return NERF_OK;
@@ -147,8 +146,8 @@ nerf_status check_distill(const char* who, int dtype, int64_t ld, int64_t n, int
     NERF_REQUIRE(ld == 0 || ld >= classes, "%s: row stride %lld below the classes", who, (long long)ld);
     NERF_REQUIRE(top >= 1 && top <= kDistillMaxTop, "%s: top %d outside 1..%d", who, top, kDistillMaxTop);
     NERF_REQUIRE(temperature > 0.0f && std::isfinite(temperature), "%s: temperature %g", who, (double)temperature);
-    if (n > kMaxItems / 256 / ((classes + 2047) / 2048))
-        return nerf_fail(NERF_ERR_UNSUPPORTED, "%s: %lld rows x %lld classes exceed one launch", who, (long long)n,
+    if (n > kMaxLogits / classes)
+        return nerf_fail(NERF_ERR_UNSUPPORTED, "%s: %lld rows x %lld classes (at most 2^40)", who, (long long)n,
                          (long long)classes);
     return NERF_OK;
 }
