@@ -1416,20 +1416,13 @@ bool direct_weights(const ExpertArgs& a) {
     return aligned16(a.x) && aligned16(a.dz) && (!a.order || a.x_rows * a.ld_x * 2 < kDirectBytes);
 }
 
-// 256 x 256 tiles of a weight gradient (one workgroup on a CU) where there is one
-// for every CU, or where an expert's sums are long enough to be split over the CUs
-// that are left; else 128 x 128 (two on a CU).  Weight gradients alone, bfloat16, us,
-// with 256 and with 128:
-//   one for every CU: 16 experts 1024 -> 4096 of 512 slots each 114 and 141, of 2048
-//   264 and 331; 64 experts 512 -> 512, 512: 37 and 48, 2048: 110 and 126; 256
-//   experts 256 -> 512, 512: 77 and 97;
-//   fewer: 16 experts 512 -> 512 of 1024 slots each 41 and 24, 2048: 52 and 41, 4096:
-//   68 and 73, 8192: 111 and 145; 8 experts 256 -> 256, 2048: 25 and 16, 4096: 25 and
-//   23, 8192: 29 and 34; 4 experts 2048 -> 1024, 2048: 55 and 48, 4096: 96 and 87; 32
-//   experts 320 -> 520, 1024: 40 and 38, 2048: 68 and 68, 4096: 122 and 134.
+// 256 x 256 tiles of a weight gradient where an expert's sums are long (2048
+// slots and more on average), else 128 x 128 (two workgroups on a CU).  Both
+// gradients of 16 experts 1024 -> 4096, 2048 slots each: 626 us against 690;
+// 64 experts 512 -> 512, 512 slots each: 115 against 100; 8 experts 256 -> 256,
+// 512 slots each: 36 against 27.
 bool wide_weight_tiles(int64_t slots, int n_experts, int d_in, int d_out) {
-    const int64_t tiles = (int64_t)n_experts * ((d_in + 255) / 256) * ((d_out + 255) / 256);
-    return d_in > 128 && d_out > 128 && (tiles >= kCus || slots / n_experts >= 4096);
+    return slots / n_experts >= 2048 && d_in > 128 && d_out > 128;
 }
 
 // Copied tiles where rows allow it, also of narrow weights (both gradients of 16
