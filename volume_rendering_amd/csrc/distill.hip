@@ -295,7 +295,8 @@ __global__ void __launch_bounds__(kSplitThreads) k_distill_part(DistillArgs a, i
     const int i = blockIdx.x % splits;
     int64_t c0, c1;
     split_range(a.classes, splits, i, c0, c1);
-    const MaxSum v = scan_row<T, kSplitThreads>((const T*)a.logits + r * a.ld, c0, c1, over_t(kLog2e, a.temperature), scratch);
+    const MaxSum v = scan_row<T, kSplitThreads>((const T*)a.logits + r * a.ld, c0, c1, over_t(kLog2e, a.temperature),
+                                                scratch);
     if (threadIdx.x == 0) {
         a.part[2 * (r * splits + i)] = v.m;
         a.part[2 * (r * splits + i) + 1] = v.s;
@@ -337,8 +338,8 @@ __global__ void __launch_bounds__(kSplitThreads) k_distill_join(DistillArgs a, i
     int64_t c0, c1;
     split_range(a.classes, gsplits, i, c0, c1);
     const float scale = a.temperature * (a.row_scale ? a.row_scale[r] : 1.0f);
-    write_grad<T, kSplitThreads>(a, top, row, (T*)a.grad + r * a.ld_grad, c0, c1, over_t(kLog2e, a.temperature), shift_of(all.m),
-                                 all.s == 0.0f ? 0.0f : 1.0f / all.s, scale);
+    write_grad<T, kSplitThreads>(a, top, row, (T*)a.grad + r * a.ld_grad, c0, c1, over_t(kLog2e, a.temperature),
+                                 shift_of(all.m), all.s == 0.0f ? 0.0f : 1.0f / all.s, scale);
 }
 
 // Gradient from a saved log-sum-exp: q = e^(z - lse).  Rounding lse, one float32
@@ -443,7 +444,8 @@ void run_grad(const DistillArgs& all, hipStream_t s) {
 // Rows are split when there are fewer than CUs, into parts of at least 2048 classes
 // and about 1024 workgroups (512 of them: the same).  Loss and gradient, bfloat16,
 // us: 64 x 128000: 16.6 split, 23.4 not; 128 x 262144: 39 and 43; 200 x 50000: 18.3
-// and 17.0; 700 x 8000: 16.4 and 12.2; 1000 x 128000: 138 and 126.
+// and 17.0 (with nearly as many rows as CUs a split loses a little); 700 x 8000:
+// 16.4 and 12.2; 1000 x 128000: 138 and 126.
 int distill_splits(int64_t n, int64_t classes) {
     if (n >= 256 || classes <= 4096) return 1;
     const int64_t most = classes / 2048, want = (1024 + n - 1) / n;

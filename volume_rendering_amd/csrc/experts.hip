@@ -43,8 +43,9 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_of(uint64_t base, int byt
 // device only, so workgroups are numbered by "virtual tiles": expert e starts
 // at tile offsets[e] / B + e.  That number never decreases, leaves room for
 // all ceil(rows / B) tiles of e, and needs no table: the expert of a tile is
-// found by a 64-way search over the offsets (one step for up to 64 experts,
-// two for up to 4096).  At most one tile an expert is empty.
+// found by a 64-way search over the offsets of the experts and of the slots
+// without one (one step for up to 63 experts, two for up to 4095, three for
+// 4096).  At most one tile an expert is empty.
 // ---------------------------------------------------------------------------
 template <class F>
 __device__ __forceinline__ int last_where(int n, F&& holds) {  // largest e < n with holds(e); holds(0) is true
@@ -480,10 +481,11 @@ __global__ void __launch_bounds__((RowsTile<T, GRAD, BM, BN, WM, WN>::NT))
 // ---------------------------------------------------------------------------
 // Forward for few slots (serving): bound by the read of the touched experts'
 // weights, and for one sample by launch and latency (1024 -> 4096 bfloat16
-// through two experts: 16.8 MB, 3.4 us at 4.9 TB/s, 8.5 us a call).  A workgroup owns 16 slots of an expert and 16 outputs; its four
-// waves take a quarter of k each, straight from memory to registers (each
-// weight is used once, so LDS would only add a step), eight loads in flight,
-// and their partial sums are added up in LDS in a fixed order.
+// through two experts: 16.8 MB, 3.4 us at 4.9 TB/s, 8.5 us a call).  A workgroup
+// owns 16 slots of an expert and 16 outputs; its four waves take a quarter of k
+// each, straight from memory to registers (each weight is used once, so LDS would
+// only add a step), eight loads in flight, and their partial sums are added up in
+// LDS in a fixed order.
 // Slots are found like tiles, or, with fewer slots than tiles, one workgroup
 // row per slot, of which those that start a tile work.
 // ---------------------------------------------------------------------------
@@ -778,8 +780,10 @@ struct TileWalk {
 // fragments' reads 210, with the stores 233; the copies into LDS, which share
 // its ports, bring the rest, and 8.5 tiles a CU run as 9.  A library product of
 // 4096 x 4096 x 4096 without routing reaches 1320 TF/s here.  256 x 256 tiles of
-// four 128 x 64 waves read least from LDS a multiplication; fewer rows a tile
-// where that fills the last round of the grid (tile_height).
+// eight 128 x 64 waves (251 registers, two waves a SIMD) read least from LDS a
+// multiplication of the shapes timed; four 128 x 128 waves would read a third less
+// and have not been.  Fewer rows a tile where that fills the last round of the grid
+// (tile_height).
 // 8 experts 256 -> 256, 262,144 slots: 74 us, bound by memory (268 MB, 55 us).
 template <bool GRAD, int BM, int BN, int WM, int WN>
 __global__ void __launch_bounds__((DirectTile<BM, BN, WM, WN, __bf16>::NT))
@@ -1362,7 +1366,10 @@ void run_few(const ExpertArgs& a, hipStream_t s) {
 //    against 56 (float32: 163 against 233), 2047 -> 63: 142 against 130 (float32: 322
 //    against 463); 1024 experts, 256 each, 64 -> 64: 36 against 76; but with 128
 //    columns, 8 experts, 32768 each, 64 -> 128: 58 against 45 (float32: 111 against
-//    89).
+//    89).  These are forward.  The gradient follows the same rule; of both gradients
+//    with 128 columns, 128 -> 128 bfloat16, one-wave tiles would take 140 against 169
+//    (8 experts, 32768 slots each), 136 against 151 (32, 8000) and 91 against 144
+//    (500, 300), float32 342 against 326, 333 against 315 and 298 against 306.
 //  - also below 256 with more than 63 experts (whose tiles have to be searched
 //    for) and at most 128 x 128 weights: 1024 experts, 64 slots each, 128 -> 128:
 //    29 against 45, 256 -> 256: 76 against 71; 256 slots each, 128 -> 128: 79
@@ -1417,10 +1424,19 @@ bool direct_weights(const ExpertArgs& a) {
 }
 
 // 256 x 256 tiles of a weight gradient where an expert's sums are long (2048
-// slots and more on average), else 128 x 128 (two workgroups on a CU).  Both
-// gradients of 16 experts 1024 -> 4096, 2048 slots each: 626 us against 690;
-// 64 experts 512 -> 512, 512 slots each: 115 against 100; 8 experts 256 -> 256,
-// 512 slots each: 36 against 27.
+// slots and more on average), else 128 x 128 (two workgroups on a CU).  The
+// weight gradient alone, bfloat16, us with 256 and with 128, of even experts | of
+// experts whose slots fall off by rank as rank^-0.7:
+//   16 experts 1024 -> 4096, 512 slots each: 113, 138 | 119, 147; 1024: 176, 210 |
+//     182, 227; 2048: 275, 344 | 284, 343;
+//   64 experts 512 -> 512, 512: 37, 47 | 77, 57; 2048: 110, 127 | 347, 236;
+//   16 experts 512 -> 512, 1024: 41, 24 | 40, 38; 2048: 52, 41 | 51, 68; 8192: 114,
+//     143 | 117, 315;
+//   8 experts 256 -> 256, 1024: 24, 15 | 23, 16; 4096: 25, 23 | 25, 24; 8192: 29, 34
+//     | 30, 34;
+//   8 experts 1024 -> 1024, 1024: 36, 31 | 47, 35; 4096: 105, 97 | 155, 121.
+// No length alone is right for all: many tiles of even experts want 256 earlier, few
+// tiles or uneven experts, whose longest decides, 128 for longer.
 bool wide_weight_tiles(int64_t slots, int n_experts, int d_in, int d_out) {
     return slots / n_experts >= 2048 && d_in > 128 && d_out > 128;
 }

@@ -23,7 +23,6 @@ enum ExpertCheckBit : unsigned {
 // ---- routing (route.hip) ----
 // Pairs one workgroup sorts; the plan's workspace holds a row of E + 1 counts
 // per workgroup and one of totals.
-constexpr int kRouteMaxExperts = 4096;
 constexpr int kRouteWaves = 8;
 constexpr int kRouteBatch = 8;  // pairs a lane holds in registers
 inline int64_t route_chunk(int64_t pairs) {
