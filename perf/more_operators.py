@@ -248,7 +248,7 @@ def prepare(case, seed):
             s["dh"] = normal(rows, d, dtype=dt)
             s["dh_last"] = normal(n, d) if case["state"] else None
         if own:
-            kw = dict(gates=g, n_seq=n, packed=case["ragged"], backward=case["dir"] == "backward")
+            kw = dict(gates=g, n_seq=n, backward=case["dir"] == "backward")
             s["ws"] = empty(max(1, v.nerf_scan_workspace_size(rows, d, **kw)), dtype=torch.uint8)
             if case["dir"] == "forward":
                 s["h"], s["h_last"] = empty(rows, d, dtype=dt), empty(n, d)
