@@ -628,6 +628,162 @@ nerf_status nerf_distill_topk_grad(const void* logits, int dtype, int64_t ld_log
                                    void* stream);
 
 /* ---------------------------------------------------------------------- */
+/* Streaming routed fields (device)                                       */
+/* ---------------------------------------------------------------------- */
+/*
+ * What a routed field needs besides its layers: the gate that picks each
+ * sample's experts, the whole two-layer field in one call for the few samples
+ * of a stream, a recurrence along the samples of a ray (or any sequence), and
+ * the norm of all its gradients.  The order of a training pass is
+ *   nerf_route_gate -> nerf_route_plan -> nerf_expert_linear (per layer)
+ *   -> nerf_route_combine -> nerf_scan,
+ * and backwards
+ *   nerf_scan_grad -> nerf_route_combine_grad -> nerf_expert_linear_grad
+ *   -> nerf_route_gate_grad (of dweights) -> nerf_grad_clip.
+ * A stream that adds a few samples at a time is served by
+ *   nerf_route_gate -> nerf_routed_mlp -> nerf_scan (sequences of length 1).
+ * Conventions as for routed fields above: dtype NERF_F32 or NERF_BF16 is the
+ * type of every `const void*`/`void*` tensor, sums and states are float32 (the
+ * gradients' norm float64) and rounded once on output, ld_* is a row stride in
+ * elements (0: contiguous), rows may start at any element, outputs must not
+ * overlap inputs unless it says so, no atomics on results: every result is the
+ * same from run to run.  A workspace serves one call at a time: calls on
+ * different streams, and captured graphs that may run at once, need their own.
+ */
+
+/* Each sample's k largest logits, largest first (the lowest expert among
+ * equals), and their softmax weights: over the chosen experts (renorm), or
+ * their probabilities among all n_experts.  An expert with logit -inf is never
+ * chosen; a choice that finds none left has id -1 and weight 0.  A NaN counts
+ * as the largest; a row with NaN or +inf has NaN weights.  logits: device
+ * [n, n_experts]; ids: device int32 [n, k]; weights: device float32 [n, k].
+ * Errors: null pointers, bad dtype or strides, k outside 1..min(64, n_experts),
+ * n*k >= 2^31; NERF_ERR_UNSUPPORTED for n_experts > 4096. */
+nerf_status nerf_route_gate(const void* logits, int dtype, int64_t ld_logits, int64_t n, int n_experts, int k,
+                            int renorm, int32_t* ids, float* weights, void* stream);
+
+/* Gradient of nerf_route_gate's weights: with S = sum_j weights_j dweights_j
+ * over the row's choices that have an expert,
+ *   renorm: dlogits_v = sum_{j: ids_j = v} weights_j (dweights_j - S)
+ *   else:   dlogits_v = sum_{j: ids_j = v} weights_j dweights_j - p_v S,  p = softmax(logits)
+ * (0 for the other experts with renorm).  Choices with an id outside
+ * [0, n_experts) count for nothing, whatever their weights hold.  logits may be
+ * NULL with renorm.  dlogits: device [n, n_experts] of dtype. */
+nerf_status nerf_route_gate_grad(const float* dweights, const void* logits, int dtype, int64_t ld_logits, int64_t n,
+                                 int n_experts, int k, int renorm, const int32_t* ids, const float* weights,
+                                 void* dlogits, int64_t ld_dlogits, void* stream);
+
+/* Pairs (sample, choice) that nerf_routed_mlp takes at most. */
+#define NERF_FEW_PAIRS 512
+
+enum {
+    NERF_ACT_NONE = 0,
+    NERF_ACT_RELU = 1,  /* max(z, 0) (a NaN stays) */
+    NERF_ACT_GATED = 2  /* z1 sigmoid(z1) z2: the first layer has 2 hidden rows, z1's before z2's */
+};
+
+typedef struct {
+    int32_t dtype;               /* of x, w1, w2 and out */
+    int32_t n_experts;           /* 1..4096 */
+    int32_t d_in, hidden, d_out; /* 1..65536 */
+    int32_t act;                 /* NERF_ACT_* of the hidden layer */
+    int32_t k;                   /* choices per sample, 1..64 */
+    int64_t ld_x, ld_out;        /* row strides (0: contiguous) */
+} nerf_routed_layer;
+
+/* Device workspace of nerf_routed_mlp (0 if the sizes are invalid). */
+size_t nerf_routed_mlp_workspace_size(int64_t n, int k, int hidden);
+
+/* A whole two-layer routed field for a few samples:
+ *   out_t = sum_j weights_tj (W2_e act(W1_e x_t + b1_e) + b2_e),  e = ids_tj,
+ * j ascending, over the choices whose id is in [0, n_experts) (0 for a sample
+ * without any; weights of the others do not matter).  x: device [n, d_in];
+ * ids: device int32 [n, k]; weights: device float32 [n, k] or NULL (all 1); w1:
+ * device [n_experts, hidden, d_in] (gated: 2 hidden rows); w2: device
+ * [n_experts, d_out, hidden]; b1, b2: device float32 [n_experts, rows] or NULL;
+ * out: device [n, d_out].  Hidden values stay in float32.  workspace: device,
+ * 16-byte aligned, at least nerf_routed_mlp_workspace_size bytes, or NULL
+ * (allocated stream-ordered).  Errors: null pointers, bad dtype, act, sizes,
+ * strides or alignment, workspace too small; NERF_ERR_UNSUPPORTED for more than
+ * 512 pairs or 4096 experts. */
+nerf_status nerf_routed_mlp(const nerf_routed_layer* layer, const void* x, const int32_t* ids, const float* weights,
+                            int64_t n, const void* w1, const float* b1, const void* w2, const float* b2, void* out,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
+/* A gated linear recurrence along packed sequences: per channel,
+ *   h_t = a_t h_{t-1} + b_t,   b_t = x_t, or (1 - a_t) x_t with mix,
+ * from h0 on, first row to last or (reverse) last to first.  With a = 1 - alpha,
+ * mix and reverse it composites any number of channels front to back: the state
+ * after a ray's first sample is its colour in front of h0.  A gate serves
+ * d / gates consecutive channels (gates = d: each its own, 1: one per row).
+ * Sequence s is rows offsets[s] .. offsets[s+1]-1, or, with offsets NULL, the
+ * s-th of n_seq equal ones; an empty one has state h0; rows outside every
+ * sequence keep what they hold.  Offsets out of range are kept in range.
+ * States are carried across runs of steps by products of their gates: those
+ * must stay in float32's range, as they do for gates of magnitude up to 1. */
+typedef struct {
+    int32_t dtype;        /* of x, h, dh and dx */
+    int32_t gate_dtype;   /* of a and da: dtype, or NERF_F32 */
+    int32_t d, gates;     /* 1..65536 channels; gates divides d */
+    int32_t reverse, mix;
+    int64_t rows, n_seq;  /* rows below 2^31 */
+    int64_t ld_a, ld_x, ld_h, ld_dh;
+} nerf_scan_cfg;
+
+/* Device workspace of nerf_scan (backward: of nerf_scan_grad); 0: none. */
+size_t nerf_scan_workspace_size(int64_t rows, int64_t n_seq, int d, int gates, int backward);
+
+/* a: device [rows, gates]; x: device [rows, d]; offsets: device int32
+ * [n_seq + 1] or NULL; h0: device float32 [n_seq, d] or NULL (0); h: device
+ * [rows, d]; h_last: device float32 [n_seq, d] or NULL, the state after each
+ * sequence; it may be h0 (a stream's state, updated in place).  Errors: null
+ * pointers, bad dtypes, sizes, strides or alignment, rows that are not n_seq
+ * equal sequences, h == x or a, workspace too small; NERF_ERR_UNSUPPORTED for
+ * bfloat16 gates of float32 rows. */
+nerf_status nerf_scan(const nerf_scan_cfg* cfg, const void* a, const void* x, const int32_t* offsets, const float* h0,
+                      void* h, float* h_last, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradients of nerf_scan from those of its outputs, dh (device [rows, d]) and
+ * dh_last (device float32 [n_seq, d] or NULL: 0).  With D_t = dh_t + a_{t+1}
+ * D_{t+1} (and dh_last at a sequence's last step):
+ *   dx_t = D_t, or (1 - a_t) D_t with mix          device [rows, d]
+ *   da_t = sum over the gate's channels D_t (h_{t-1} [- x_t with mix])  device [rows, gates]
+ *   dh0 = a_1 D_1 (dh_last if empty)                device float32 [n_seq, d], or NULL
+ * a, x, offsets, h0 as given to nerf_scan, h as it returned it; x may be NULL
+ * without mix.  dh0 may be dh_last.  da and dx are contiguous. */
+nerf_status nerf_scan_grad(const nerf_scan_cfg* cfg, const void* dh, const float* dh_last, const void* a,
+                           const void* x, const void* h, const float* h0, const int32_t* offsets, void* da, void* dx,
+                           float* dh0, void* workspace, size_t workspace_bytes, void* stream);
+
+/* One tensor of a list of gradients (the list itself is host memory). */
+typedef struct {
+    const void* src;  /* device, contiguous, aligned to its elements */
+    void* dst;        /* where nerf_grad_clip writes: src itself, or other memory */
+    int64_t count;    /* elements */
+    int32_t dtype;
+    int32_t reserved;
+} nerf_tensor;
+
+/* Device workspace of nerf_grad_norm and nerf_grad_clip for this list. */
+size_t nerf_grad_norm_workspace_size(const nerf_tensor* list, int n);
+
+/* norm = sqrt(sum of g^2 over every element of every tensor): device float32
+ * [1].  The sum is float64 in a fixed order.  No tensors, or only empty ones:
+ * 0.  workspace: device, 16-byte aligned, or NULL (allocated stream-ordered).
+ * Errors: null pointers, bad dtype, count or alignment, more than 2^20 tensors
+ * or 2^41 elements, workspace too small. */
+nerf_status nerf_grad_norm(const nerf_tensor* list, int n, float* norm, void* workspace, size_t workspace_bytes,
+                           void* stream);
+
+/* norm as above, and dst = src * min(1, max_norm / norm) for every tensor.  A
+ * NaN norm makes every element NaN; with an infinite one finite elements become
+ * 0.  Tensors scaled in place by 1 are not touched.  Errors: as nerf_grad_norm,
+ * a NULL destination, max_norm negative or NaN, a destination that overlaps
+ * another tensor's source or destination, or its own source in part. */
+nerf_status nerf_grad_clip(const nerf_tensor* list, int n, float max_norm, float* norm, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------- */
 /* For callers that cannot allocate                                       */
 /* ---------------------------------------------------------------------- */
 

@@ -22,6 +22,8 @@ NERF_F32, NERF_BF16 = 0, 1
 NERF_NET_8x256, NERF_NET_4x64, NERF_NET_CELL_2x32, NERF_NET_HASH_FIELD = 1, 2, 3, 4
 NERF_MODE_NERF, NERF_MODE_HASH, NERF_MODE_KILO = 0, 1, 2
 HASH_MAX_LEVELS = 16
+NERF_FEW_PAIRS = 512
+_ACTS = {"none": 0, "relu": 1, "gated": 2}
 
 EXPORTED = [
     "nerf_abi_version", "nerf_status_str", "nerf_last_error", "nerf_hashgrid_init", "nerf_mlp_packed_bytes",
@@ -32,7 +34,9 @@ EXPORTED = [
     "nerf_hash_inr_train_step", "nerf_check_flags", "nerf_route_workspace_size", "nerf_route_plan",
     "nerf_route_gather", "nerf_route_combine", "nerf_route_combine_grad", "nerf_expert_linear",
     "nerf_expert_linear_grad_workspace_size", "nerf_expert_linear_grad", "nerf_distill_workspace_size",
-    "nerf_distill_topk", "nerf_distill_topk_grad",
+    "nerf_distill_topk", "nerf_distill_topk_grad", "nerf_route_gate", "nerf_route_gate_grad",
+    "nerf_routed_mlp_workspace_size", "nerf_routed_mlp", "nerf_scan_workspace_size", "nerf_scan", "nerf_scan_grad",
+    "nerf_grad_norm_workspace_size", "nerf_grad_norm", "nerf_grad_clip",
 ]
 
 
@@ -89,6 +93,22 @@ class nerf_hash_inr_cfg(C.Structure):
                 ("beta2", C.c_float), ("eps", C.c_float)]
 
 
+class nerf_routed_layer(C.Structure):
+    _fields_ = [("dtype", C.c_int32), ("n_experts", C.c_int32), ("d_in", C.c_int32), ("hidden", C.c_int32),
+                ("d_out", C.c_int32), ("act", C.c_int32), ("k", C.c_int32), ("ld_x", C.c_int64), ("ld_out", C.c_int64)]
+
+
+class nerf_scan_cfg(C.Structure):
+    _fields_ = [("dtype", C.c_int32), ("gate_dtype", C.c_int32), ("d", C.c_int32), ("gates", C.c_int32),
+                ("reverse", C.c_int32), ("mix", C.c_int32), ("rows", C.c_int64), ("n_seq", C.c_int64),
+                ("ld_a", C.c_int64), ("ld_x", C.c_int64), ("ld_h", C.c_int64), ("ld_dh", C.c_int64)]
+
+
+class nerf_tensor(C.Structure):
+    _fields_ = [("src", C.c_void_p), ("dst", C.c_void_p), ("count", C.c_int64), ("dtype", C.c_int32),
+                ("reserved", C.c_int32)]
+
+
 def lib():
     """The loaded library; raises if it has not been built."""
     global _lib
@@ -137,6 +157,16 @@ def lib():
             "nerf_distill_workspace_size": (S, [I64, I64]),
             "nerf_distill_topk": (I, [P, I, I64, I64, I64, P, P, I, C.c_float, P, P, P, P, I64, P, S, P]),
             "nerf_distill_topk_grad": (I, [P, I, I64, I64, I64, P, P, I, C.c_float, P, P, P, I64, P]),
+            "nerf_route_gate": (I, [P, I, I64, I64, I, I, I, P, P, P]),
+            "nerf_route_gate_grad": (I, [P, P, I, I64, I64, I, I, I, P, P, P, I64, P]),
+            "nerf_routed_mlp_workspace_size": (S, [I64, I, I]),
+            "nerf_routed_mlp": (I, [C.POINTER(nerf_routed_layer), P, P, P, I64, P, P, P, P, P, P, S, P]),
+            "nerf_scan_workspace_size": (S, [I64, I64, I, I, I]),
+            "nerf_scan": (I, [C.POINTER(nerf_scan_cfg), P, P, P, P, P, P, P, S, P]),
+            "nerf_scan_grad": (I, [C.POINTER(nerf_scan_cfg), P, P, P, P, P, P, P, P, P, P, P, S, P]),
+            "nerf_grad_norm_workspace_size": (S, [P, I]),
+            "nerf_grad_norm": (I, [P, I, P, P, S, P]),
+            "nerf_grad_clip": (I, [P, I, C.c_float, P, P, S, P]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -562,3 +592,187 @@ def nerf_distill_topk_grad(logits, t_logits, t_ids, temperature, lse, grad, row_
     _check(lib().nerf_distill_topk_grad(*args, _tensor(lse, "lse", torch.float32, (logits.shape[0],)),
                                         _tensor(grad, "grad", logits.dtype, logits.shape, True), _ld(grad),
                                         _stream_handle()), "nerf_distill_topk_grad")
+
+
+# ----------------------------------------------------------------------------
+# Streaming routed fields
+# ----------------------------------------------------------------------------
+
+def _here(*tensors):
+    """Refuses tensors of another device than the current one, on whose
+    stream the call would run."""
+    now = _torch().cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != now:
+            raise NerfError(f"tensor on {t.device}, but the current device is cuda:{now}")
+
+
+def nerf_route_gate(logits, ids, weights, renorm=True):
+    """Each sample's k largest of ``logits`` [n, experts] (rows may be
+    strided): writes int32 ``ids`` [n, k], largest first, -1 where no expert is
+    left (-inf), and float32 ``weights`` [n, k], a softmax over the chosen
+    (``renorm``) or over all experts."""
+    torch = _torch()
+    n, E = _matrix(logits, "logits")
+    k = _matrix(ids, "ids")[1]
+    args = (_tensor(logits, "logits", logits.dtype, (n, E), True), _dtype_of(logits, "logits"), _ld(logits), n, E, k,
+            int(renorm), _tensor(ids, "ids", torch.int32, (n, k)), _tensor(weights, "weights", torch.float32, (n, k)))
+    _here(logits, ids, weights)
+    _check(lib().nerf_route_gate(*args, _stream_handle()), "nerf_route_gate")
+
+
+def nerf_route_gate_grad(dweights, logits, ids, weights, dlogits, renorm=True):
+    """Gradient of nerf_route_gate: ``dlogits`` [n, experts] from ``dweights``
+    float32 [n, k] and the call's ``ids`` and ``weights``.  ``logits`` may be
+    None with ``renorm``.  Rows of ``logits`` and ``dlogits`` may be strided."""
+    torch = _torch()
+    n, E = _matrix(dlogits, "dlogits")
+    k = _matrix(ids, "ids")[1]
+    dt, f32 = dlogits.dtype, torch.float32
+    args = (_tensor(dweights, "dweights", f32, (n, k)), _tensor(logits, "logits", dt, (n, E), True),
+            _dtype_of(dlogits, "dlogits"), _ld(logits), n, E, k, int(renorm), _tensor(ids, "ids", torch.int32, (n, k)),
+            _tensor(weights, "weights", f32, (n, k)), _tensor(dlogits, "dlogits", dt, (n, E), True), _ld(dlogits))
+    _here(dweights, logits, ids, weights, dlogits)
+    _check(lib().nerf_route_gate_grad(*args, _stream_handle()), "nerf_route_gate_grad")
+
+
+def nerf_routed_mlp_workspace_size(n: int, k: int, hidden: int) -> int:
+    return lib().nerf_routed_mlp_workspace_size(n, k, hidden)
+
+
+def nerf_routed_mlp(x, ids, weights, w1, b1, w2, b2, out, act="relu", workspace=None):
+    """A whole two-layer routed field for a few samples (n k up to 512):
+    out[t] = sum_j weights[t, j] (W2_e act(W1_e x[t] + b1_e) + b2_e), e = ids[t, j].
+    ``x`` [n, d_in] and ``out`` [n, d_out] (rows may be strided), ``ids`` int32
+    [n, k] (outside the experts: no expert), ``weights`` float32 [n, k] or None
+    (all 1), ``w1`` [E, hidden, d_in] ([E, 2 hidden, d_in] with act "gated"),
+    ``w2`` [E, d_out, hidden], ``b1`` and ``b2`` float32 or None.  ``act``:
+    "none", "relu" or "gated" (z1 sigmoid(z1) z2, z1's rows first)."""
+    torch = _torch()
+    if act not in _ACTS:
+        raise NerfError(f"act: {act!r}, expected one of {sorted(_ACTS)}")
+    if w1.dim() != 3 or w2.dim() != 3:
+        raise NerfError(f"w1 and w2: {w1.dim()} and {w2.dim()} dimensions, expected 3")
+    E, d_out, hidden = w2.shape
+    (n, d_in), k = _matrix(x, "x"), _matrix(ids, "ids")[1]
+    up = 2 * hidden if act == "gated" else hidden
+    dt, f32 = x.dtype, torch.float32
+    L = nerf_routed_layer(_dtype_of(x, "x"), E, d_in, hidden, d_out, _ACTS[act], k, _ld(x), _ld(out))
+    ws, wsb = _ws(workspace)
+    args = (_tensor(x, "x", dt, (n, d_in), True), _tensor(ids, "ids", torch.int32, (n, k)),
+            _tensor(weights, "weights", f32, (n, k)), n, _tensor(w1, "w1", dt, (E, up, d_in)),
+            _tensor(b1, "b1", f32, (E, up)), _tensor(w2, "w2", dt, (E, d_out, hidden)),
+            _tensor(b2, "b2", f32, (E, d_out)), _tensor(out, "out", dt, (n, d_out), True))
+    _here(x, ids, weights, w1, b1, w2, b2, out, workspace)
+    _check(lib().nerf_routed_mlp(C.byref(L), *args, ws, wsb, _stream_handle()), "nerf_routed_mlp")
+
+
+def nerf_scan_workspace_size(rows: int, d: int, gates=None, n_seq: int = 1, backward: bool = False) -> int:
+    return lib().nerf_scan_workspace_size(rows, n_seq, d, d if gates is None else gates, int(backward))
+
+
+def _scan_cfg(a, x, offsets, n_seq, reverse, mix, ld_x, ld_h, ld_dh=0):
+    """The call's configuration from its gates and one [rows, d] tensor, and
+    the number of sequences."""
+    rows, d = _matrix(x, "x")
+    gates = _matrix(a, "a")[1]
+    if offsets is not None:
+        n_seq = offsets.numel() - 1
+    elif n_seq is None:
+        n_seq = 1
+    return nerf_scan_cfg(_dtype_of(x, "x"), _dtype_of(a, "a"), d, gates, int(reverse), int(mix), rows, n_seq, _ld(a),
+                         ld_x, ld_h, ld_dh), rows, d, gates, n_seq
+
+
+def nerf_scan(a, x, h, h0=None, h_last=None, offsets=None, n_seq=None, reverse=False, mix=False, workspace=None):
+    """The recurrence h_t = a_t h_{t-1} + x_t (``mix``: + (1 - a_t) x_t) along
+    packed sequences: ``x`` and ``h`` [rows, d], ``a`` [rows, gates] (gates
+    divides d; x's type or float32), rows may be strided.  Sequences are given
+    by int32 ``offsets`` [n_seq + 1], or are ``n_seq`` equal ones (1).
+    ``reverse``: from the last row to the first.  ``h0`` float32 [n_seq, d] or
+    None (0); ``h_last`` float32 [n_seq, d] or None, may be ``h0``."""
+    torch = _torch()
+    cfg, rows, d, gates, n_seq = _scan_cfg(a, x, offsets, n_seq, reverse, mix, _ld(x), _ld(h))
+    f32 = torch.float32
+    ws, wsb = _ws(workspace)
+    args = (_tensor(a, "a", a.dtype, (rows, gates), True), _tensor(x, "x", x.dtype, (rows, d), True),
+            _tensor(offsets, "offsets", torch.int32, (n_seq + 1,)), _tensor(h0, "h0", f32, (n_seq, d)),
+            _tensor(h, "h", x.dtype, (rows, d), True), _tensor(h_last, "h_last", f32, (n_seq, d)))
+    _here(a, x, offsets, h0, h, h_last, workspace)
+    _check(lib().nerf_scan(C.byref(cfg), *args, ws, wsb, _stream_handle()), "nerf_scan")
+
+
+def nerf_scan_grad(dh, a, x, h, da, dx, h0=None, dh_last=None, dh0=None, offsets=None, n_seq=None, reverse=False,
+                   mix=False, workspace=None):
+    """Gradients of nerf_scan from ``dh`` [rows, d] and ``dh_last`` float32
+    [n_seq, d] or None (0): contiguous ``da`` [rows, gates] and ``dx`` [rows, d],
+    and ``dh0`` float32 [n_seq, d] or None (may be ``dh_last``).  ``h`` is the
+    forward call's result; ``x`` may be None without ``mix``."""
+    torch = _torch()
+    cfg, rows, d, gates, n_seq = _scan_cfg(a, dh, offsets, n_seq, reverse, mix, _ld(x), _ld(h), _ld(dh))
+    f32, dt = torch.float32, dh.dtype
+    ws, wsb = _ws(workspace)
+    args = (_tensor(dh, "dh", dt, (rows, d), True), _tensor(dh_last, "dh_last", f32, (n_seq, d)),
+            _tensor(a, "a", a.dtype, (rows, gates), True), _tensor(x, "x", dt, (rows, d), True),
+            _tensor(h, "h", dt, (rows, d), True), _tensor(h0, "h0", f32, (n_seq, d)),
+            _tensor(offsets, "offsets", torch.int32, (n_seq + 1,)), _tensor(da, "da", a.dtype, (rows, gates)),
+            _tensor(dx, "dx", dt, (rows, d)), _tensor(dh0, "dh0", f32, (n_seq, d)))
+    _here(dh, dh_last, a, x, h, h0, offsets, da, dx, dh0, workspace)
+    _check(lib().nerf_scan_grad(C.byref(cfg), *args, ws, wsb, _stream_handle()), "nerf_scan_grad")
+
+
+class _TensorList:
+    """A host list of tensors for nerf_grad_norm and nerf_grad_clip; it keeps
+    them alive."""
+
+    def __init__(self, tensors, outs):
+        self.tensors, self.outs = list(tensors), None if outs is None else list(outs)
+        if self.outs is not None and len(self.outs) != len(self.tensors):
+            raise NerfError(f"{len(self.tensors)} tensors, {len(self.outs)} outputs")
+        self.n = len(self.tensors)
+        self.array = (nerf_tensor * max(1, self.n))()
+        self.device = self.tensors[0].device.index if self.tensors else None
+        for i, t in enumerate(self.tensors):
+            o = t if self.outs is None else self.outs[i]
+            src = _tensor(t, f"tensor {i}", t.dtype, t.shape)
+            self.array[i] = nerf_tensor(src, _tensor(o, f"output {i}", t.dtype, t.shape), t.numel(),
+                                        _dtype_of(t, f"tensor {i}"), 0)
+            if t.device.index != self.device or o.device.index != self.device:
+                raise NerfError(f"tensor {i}: not on cuda:{self.device} as the first")
+
+
+def nerf_tensor_list(tensors, outs=None) -> _TensorList:
+    """The list that nerf_grad_norm and nerf_grad_clip take: contiguous float32
+    or bfloat16 device ``tensors``, and the tensors of the same types and shapes
+    that clipping writes (None: in place).  Built once, it serves every step in
+    which the tensors stay where they are."""
+    return _TensorList(tensors, outs)
+
+
+def nerf_grad_norm_workspace_size(tensors) -> int:
+    return lib().nerf_grad_norm_workspace_size(C.byref(tensors.array), tensors.n)
+
+
+def _norm_args(tensors, norm, workspace):
+    torch = _torch()
+    ws, wsb = _ws(workspace)
+    p = _tensor(norm, "norm", torch.float32, (1,))
+    _here(norm, workspace)
+    if tensors.n and tensors.device != norm.device.index:
+        raise NerfError(f"tensors on cuda:{tensors.device}, but the current device is {norm.device}")
+    return p, ws, wsb
+
+
+def nerf_grad_norm(tensors, norm, workspace=None):
+    """``norm`` (float32 [1]) of every element of every tensor of a
+    nerf_tensor_list."""
+    p, ws, wsb = _norm_args(tensors, norm, workspace)
+    _check(lib().nerf_grad_norm(C.byref(tensors.array), tensors.n, p, ws, wsb, _stream_handle()), "nerf_grad_norm")
+
+
+def nerf_grad_clip(tensors, max_norm: float, norm, workspace=None):
+    """Scales every tensor of a nerf_tensor_list by min(1, max_norm / norm) into
+    its output, and writes the ``norm`` from before (float32 [1])."""
+    p, ws, wsb = _norm_args(tensors, norm, workspace)
+    _check(lib().nerf_grad_clip(C.byref(tensors.array), tensors.n, float(max_norm), p, ws, wsb, _stream_handle()),
+           "nerf_grad_clip")

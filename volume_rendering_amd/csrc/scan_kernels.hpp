@@ -1,0 +1,452 @@
+// The gated linear recurrence and its gradient for gfx950.  Along a sequence,
+// per channel,
+//   h_t = a_t h_{t-1} + b_t,      b_t = x_t, or (1 - a_t) x_t  (mix)
+// and, with D_t = dh_t + a_{t+1} D_{t+1} the whole gradient at h_t (D_T has
+// dh_last added),
+//   dx_t = D_t [(1 - a_t)],   da_t = sum over the gate's channels D_t (h_{t-1} [- x_t]),   dh0 = a_1 D_1.
+// Both are recurrences s' = A s + B: the forward one with (a_t, b_t), the
+// gradient against the sequence with (a_t, a_t dh_t) on what flows into h_t
+// from behind.  n steps are again such a step, with the product of their A and
+// the state that they reach from 0; so a wave's lanes take runs of kSteps
+// consecutive steps each, join the runs by a scan of those pairs, and then walk
+// their own steps from the true state before them.  Products of gates only
+// carry states from run to run; within a run the recurrence itself is applied.
+//
+// Bound by memory: x, a and h once each (the gradient: dh, a, h and the
+// outputs).  A workgroup walks one sequence for a block of channels, tile by
+// tile, with the tile's loads all in flight at once.  When sequences are too
+// few for that to fill the card they are split into chunks, and the chunks' sums
+// found first: x and a are then read twice.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <type_traits>
+
+#include "common.hpp"
+#include "fields.hpp"
+
+namespace nerf {
+
+namespace {
+
+constexpr int kSteps = 8;         // steps of a lane's run
+constexpr int kScanGrid = 1 << 20;
+
+// V consecutive elements at any element alignment (global memory takes wide
+// accesses at any address here).
+template <class T, int V>
+struct Some {
+    struct __attribute__((packed, aligned(sizeof(T)))) Raw {
+        T e[V];
+    };
+    static __device__ __forceinline__ void load(float (&f)[V], const T* p) {
+        const Raw r = *reinterpret_cast<const Raw*>(p);
+#pragma unroll
+        for (int v = 0; v < V; ++v) f[v] = (float)r.e[v];
+    }
+    // elements from `skip` on
+    static __device__ __forceinline__ void store(T* p, const float (&f)[V], int skip) {
+        Raw r;
+#pragma unroll
+        for (int v = 0; v < V; ++v) r.e[v] = (T)f[v];
+        if (skip == 0) {
+            *reinterpret_cast<Raw*>(p) = r;
+        } else {
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                if (v >= skip) p[v] = r.e[v];
+        }
+    }
+};
+
+// What a workgroup (or, of single waves, a wave) works on: steps [c0, c1) of a
+// sequence of `len`, whose step i is row first + i step, for channels from
+// block on.
+struct ScanUnit {
+    int64_t seq, first, len, c0, c1, slot;
+    int step, block;
+};
+
+__device__ __forceinline__ int64_t clamp_row(int64_t v, int64_t rows) { return v < 0 ? 0 : v > rows ? rows : v; }
+
+__device__ __forceinline__ void sequence_rows(const ScanArgs& a, int64_t seq, int64_t& lo, int64_t& len) {
+    if (a.offsets) {
+        const int64_t o0 = a.offsets[seq], o1 = a.offsets[seq + 1];
+        NERF_DCHECK(o0 >= 0 && o1 >= o0 && o1 <= a.rows, kCheckScanOffset);
+        lo = clamp_row(o0, a.rows);
+        const int64_t hi = clamp_row(o1, a.rows);
+        len = hi > lo ? hi - lo : 0;
+    } else {
+        lo = seq * a.len;
+        len = a.len;
+    }
+}
+
+// First chunk of a sequence: of equal ones their number each, else at most one
+// more than the whole chunks in front (room for every sequence's partial one).
+__device__ __forceinline__ int64_t first_slot(const ScanArgs& a, int64_t seq) {
+    if (!a.offsets) return seq * ((a.len + a.p.chunk - 1) / a.p.chunk);
+    return clamp_row(a.offsets[seq], a.rows) / a.p.chunk + seq;
+}
+
+// Unit `u` of a call that walks whole sequences (chunk 0), or of one chunk
+// each; false if there is nothing to do.
+__device__ __forceinline__ bool scan_unit(const ScanArgs& a, int64_t u, bool against, ScanUnit& r) {
+    int64_t lo;
+    r.block = (int)(u % a.p.blocks);
+    u /= a.p.blocks;
+    r.slot = u;
+    if (a.p.chunk == 0) {
+        r.seq = u;
+        sequence_rows(a, u, lo, r.len);
+        r.c0 = 0;
+        r.c1 = r.len;
+    } else {
+        int64_t i;
+        if (a.offsets) {  // the last sequence whose first chunk is at or before u
+            int64_t s0 = 0, s1 = a.n_seq - 1;
+            while (s0 < s1) {
+                const int64_t mid = (s0 + s1 + 1) / 2;
+                if (first_slot(a, mid) <= u)
+                    s0 = mid;
+                else
+                    s1 = mid - 1;
+            }
+            r.seq = s0;
+            i = u - first_slot(a, s0);
+        } else {
+            const int64_t per = (a.len + a.p.chunk - 1) / a.p.chunk;
+            r.seq = u / per;
+            i = u % per;
+            if (r.seq >= a.n_seq) return false;
+        }
+        sequence_rows(a, r.seq, lo, r.len);
+        r.c0 = i * a.p.chunk;
+        if (i < 0 || r.c0 >= r.len) return false;
+        r.c1 = r.c0 + a.p.chunk < r.len ? r.c0 + a.p.chunk : r.len;
+    }
+    r.step = (a.reverse != 0) != against ? -1 : 1;
+    r.first = r.step > 0 ? lo : lo + r.len - 1;
+    return true;
+}
+
+// A lane's channels.  It has V of them from `c` on, of which those before
+// `skip` belong to its neighbour (the last lane of a width that is no multiple
+// of V starts earlier); none of them if !live.
+struct ScanLane {
+    int c, gate, skip;
+    bool live;
+};
+template <int V, bool GROUPED>
+__device__ __forceinline__ ScanLane scan_lane(const ScanArgs& a, int block, int cl) {
+    ScanLane r;
+    if constexpr (GROUPED) {
+        const int m = a.d / a.gates, lg = a.p.lg, per = a.p.cl / lg;  // gates side by side in a block
+        const int in = cl % lg + block % a.p.parts * lg;              // lane of the gate's channels
+        r.gate = block / a.p.parts * per + cl / lg;
+        const int want = in * V;
+        r.live = r.gate < a.gates && want < m;
+        const int c = want + V <= m ? want : m - V;
+        r.skip = r.live ? want - c : V;
+        if (r.gate >= a.gates) r.gate = a.gates - 1;
+        r.c = r.gate * m + c;
+    } else {
+        const int64_t want = ((int64_t)block * a.p.cl + cl) * V;
+        r.live = want < a.d;
+        r.c = want + V <= a.d ? (int)want : a.d - V;
+        r.skip = r.live ? (int)want - r.c : V;
+        r.gate = r.c;
+    }
+    return r;
+}
+
+// s' = A s + B for a lane's channels: NA is V, or 1 where they share a gate.
+template <int NA, int V>
+struct Affine {
+    float A[NA], B[V];
+};
+template <int NA, int V>
+__device__ __forceinline__ Affine<NA, V> after(const Affine<NA, V>& first, const Affine<NA, V>& then) {
+    Affine<NA, V> r;
+#pragma unroll
+    for (int v = 0; v < V; ++v) r.B[v] = fmaf(then.A[NA == 1 ? 0 : v], first.B[v], then.B[v]);
+#pragma unroll
+    for (int v = 0; v < NA; ++v) r.A[v] = then.A[v] * first.A[v];
+    return r;
+}
+
+enum ScanPhase { kScanWhole = 0, kScanSums = 1, kScanApply = 2 };
+
+// Sums over lg lanes (a power of two) of kSteps values each; the lane's own
+// steps' sums are left in every lane.
+__device__ __forceinline__ void sum_over(float (&v)[kSteps], int lg) {
+    for (int off = lg / 2; off >= 1; off >>= 1)
+#pragma unroll
+        for (int j = 0; j < kSteps; ++j) v[j] += __shfl_xor(v[j], off, 64);
+}
+
+// TA, T: types of the gates and of the rows; V channels a lane; W waves share a
+// unit (1: each wave has its own); S steps a lane (kSteps, or 1 where sequences
+// are that short); BACK: the gradient.
+template <class TA, class T, int V, bool GROUPED, int W, int S, bool BACK>
+__global__ void __launch_bounds__(W == 1 ? 256 : 64 * W) k_scan(ScanArgs a, int64_t units, int phase) {
+    constexpr int NA = GROUPED ? 1 : V;
+    using Aff = Affine<NA, V>;
+    __shared__ Aff total[W == 1 ? 1 : 2][W][W == 1 ? 1 : 64];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int CL = a.p.cl, TL = 64 / CL, cl = lane % CL, tl = lane / CL;
+    const int64_t tile = (int64_t)W * TL * S;
+    const T* const in = (const T*)(BACK ? a.dh : a.x);
+    const int64_t ld_in = BACK ? a.ld_dh : a.ld_x;
+    int turn = 0;
+    for (int64_t u = W == 1 ? (int64_t)blockIdx.x * 4 + wave : blockIdx.x; u < units;
+         u += W == 1 ? (int64_t)gridDim.x * 4 : gridDim.x) {
+        ScanUnit q;
+        if (!scan_unit(a, u, BACK, q)) continue;
+        const ScanLane ch = scan_lane<V, GROUPED>(a, q.block, cl);
+        // the state before the unit's first step
+        float s[V];
+        {
+            const float* const from = phase == kScanApply ? a.sum_a + q.slot * a.d
+                                      : phase == kScanSums ? nullptr
+                                      : BACK ? (a.dh_last ? a.dh_last + q.seq * a.d : nullptr)
+                                             : (a.h0 ? a.h0 + q.seq * a.d : nullptr);
+#pragma unroll
+            for (int v = 0; v < V; ++v) s[v] = 0.0f;
+            if (from) Some<float, V>::load(s, from + ch.c);
+        }
+        float first_h[V];  // gradient: the state before the sequence
+        if constexpr (BACK) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) first_h[v] = 0.0f;
+            if (a.h0 && phase != kScanSums) Some<float, V>::load(first_h, a.h0 + q.seq * a.d + ch.c);
+        }
+        float product[NA];
+#pragma unroll
+        for (int v = 0; v < NA; ++v) product[v] = 1.0f;
+
+        for (int64_t t0 = q.c0; t0 < q.c1; t0 += tile) {
+            const int64_t i0 = t0 + ((int64_t)(W == 1 ? 0 : wave) * TL + tl) * S;  // this lane's first step
+            const int64_t left = q.c1 - i0;                          // its steps: min(left, S), none if <= 0
+            // Loads of steps past the end repeat the last one's.
+            float ga[S][NA], gi[S][V];
+            auto row = [&](int j) {
+                const int64_t i = j < left ? i0 + j : q.c1 - 1;
+                return q.first + i * q.step;
+            };
+#pragma unroll
+            for (int j = 0; j < S; ++j) {
+                const int64_t r = row(j);
+                Some<TA, NA>::load(ga[j], (const TA*)a.a + r * a.ld_a + ch.gate);
+                Some<T, V>::load(gi[j], in + r * ld_in + ch.c);
+            }
+            float hp[BACK ? S : 1][V], xs[BACK ? S : 1][V];
+            if constexpr (BACK) {
+                if (phase != kScanSums) {
+#pragma unroll
+                    for (int j = 0; j < S; ++j) {
+                        const int64_t i = j < left ? i0 + j : q.c1 - 1, next = i + 1 < q.len ? i + 1 : i;
+                        Some<T, V>::load(hp[j], (const T*)a.h + (q.first + next * q.step) * a.ld_h + ch.c);
+                        if (i + 1 == q.len)
+#pragma unroll
+                            for (int v = 0; v < V; ++v) hp[j][v] = first_h[v];
+                        if (a.mix) {
+                            Some<T, V>::load(xs[j], (const T*)a.x + (q.first + i * q.step) * a.ld_x + ch.c);
+#pragma unroll
+                            for (int v = 0; v < V; ++v) hp[j][v] -= xs[j][v];
+                        }
+                    }
+                }
+            } else if (a.mix) {
+#pragma unroll
+                for (int j = 0; j < S; ++j)
+#pragma unroll
+                    for (int v = 0; v < V; ++v) gi[j][v] *= 1.0f - ga[j][NA == 1 ? 0 : v];
+            }
+            // the lane's run as one step
+            Aff run;
+#pragma unroll
+            for (int v = 0; v < NA; ++v) run.A[v] = 1.0f;
+#pragma unroll
+            for (int v = 0; v < V; ++v) run.B[v] = 0.0f;
+#pragma unroll
+            for (int j = 0; j < S; ++j)
+                if (j < left) {
+#pragma unroll
+                    for (int v = 0; v < V; ++v) {
+                        const float A = ga[j][NA == 1 ? 0 : v];
+                        run.B[v] = BACK ? A * (run.B[v] + gi[j][v]) : fmaf(A, run.B[v], gi[j][v]);
+                    }
+#pragma unroll
+                    for (int v = 0; v < NA; ++v) run.A[v] *= ga[j][v];
+                }
+            // runs of the wave's lanes of the same channels, in order
+            for (int off = CL; off < 64; off <<= 1) {
+                Aff o;
+#pragma unroll
+                for (int v = 0; v < NA; ++v) o.A[v] = __shfl_up(run.A[v], off, 64);
+#pragma unroll
+                for (int v = 0; v < V; ++v) o.B[v] = __shfl_up(run.B[v], off, 64);
+                if (lane >= off) run = after(o, run);
+            }
+            Aff all, before;  // the wave's steps; those of the lanes before
+#pragma unroll
+            for (int v = 0; v < NA; ++v) {
+                all.A[v] = __shfl(run.A[v], 64 - CL + cl, 64);
+                const float A = __shfl_up(run.A[v], CL, 64);
+                before.A[v] = tl == 0 ? 1.0f : A;
+            }
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                all.B[v] = __shfl(run.B[v], 64 - CL + cl, 64);
+                const float B = __shfl_up(run.B[v], CL, 64);
+                before.B[v] = tl == 0 ? 0.0f : B;
+            }
+            // the state before the wave's first step, and after the tile
+            float mine[V];
+            if constexpr (W == 1) {
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    mine[v] = s[v];
+                    s[v] = fmaf(all.A[NA == 1 ? 0 : v], s[v], all.B[v]);
+                }
+                if (phase == kScanSums)
+#pragma unroll
+                    for (int v = 0; v < NA; ++v) product[v] *= all.A[v];
+            } else {
+                // (two buffers in turn: a wave is at most one tile ahead of the slowest)
+                if (tl == 0) total[turn][wave][cl] = all;
+                __syncthreads();
+#pragma unroll
+                for (int w = 0; w < W; ++w) {
+                    const Aff o = total[turn][w][cl];
+#pragma unroll
+                    for (int v = 0; v < V; ++v) {
+                        if (w == wave) mine[v] = s[v];
+                        s[v] = fmaf(o.A[NA == 1 ? 0 : v], s[v], o.B[v]);
+                    }
+                    if (phase == kScanSums)
+#pragma unroll
+                        for (int v = 0; v < NA; ++v) product[v] *= o.A[v];
+                }
+                turn ^= 1;
+            }
+            if (phase == kScanSums) continue;
+#pragma unroll
+            for (int v = 0; v < V; ++v) mine[v] = fmaf(before.A[NA == 1 ? 0 : v], mine[v], before.B[v]);
+            // the steps themselves
+            if constexpr (!BACK) {
+#pragma unroll
+                for (int j = 0; j < S; ++j) {
+#pragma unroll
+                    for (int v = 0; v < V; ++v) mine[v] = fmaf(ga[j][NA == 1 ? 0 : v], mine[v], gi[j][v]);
+                    if (j < left && ch.live)
+                        Some<T, V>::store((T*)a.h + (q.first + (i0 + j) * q.step) * a.ld_h + ch.c, mine, ch.skip);
+                }
+            } else {
+                float sum[kSteps];
+#pragma unroll
+                for (int j = 0; j < S; ++j) {
+                    const int64_t r = q.first + (i0 + j) * q.step;
+                    float dx[V], da[V];
+#pragma unroll
+                    for (int v = 0; v < V; ++v) {
+                        const float A = ga[j][NA == 1 ? 0 : v], D = gi[j][v] + mine[v];
+                        dx[v] = a.mix ? (1.0f - A) * D : D;
+                        da[v] = D * hp[j][v];
+                        mine[v] = A * D;
+                    }
+                    if (j < left && ch.live) {
+                        Some<T, V>::store((T*)a.dx + r * a.d + ch.c, dx, ch.skip);
+                        if constexpr (!GROUPED) Some<TA, V>::store((TA*)a.da + r * a.gates + ch.c, da, ch.skip);
+                    }
+                    if constexpr (GROUPED) {
+                        sum[j] = 0.0f;
+#pragma unroll
+                        for (int v = 0; v < V; ++v) sum[j] += ch.live && v >= ch.skip ? da[v] : 0.0f;
+                    }
+                }
+                if constexpr (GROUPED) {
+#pragma unroll
+                    for (int j = S; j < kSteps; ++j) sum[j] = 0.0f;
+                    sum_over(sum, a.p.lg);
+                    if (ch.live && cl % a.p.lg == 0)
+#pragma unroll
+                        for (int j = 0; j < S; ++j)
+                            if (j < left) {
+                                const int64_t r = q.first + (i0 + j) * q.step;
+                                if (a.p.parts > 1)
+                                    a.part_da[((int64_t)(q.block % a.p.parts) * a.rows + r) * a.gates + ch.gate] = sum[j];
+                                else
+                                    ((TA*)a.da)[r * a.gates + ch.gate] = (TA)sum[j];
+                            }
+                }
+            }
+        }
+        // (every wave has the state after the last tile)
+        if (ch.live && tl == 0 && (W == 1 || wave == 0)) {
+            if (phase == kScanSums) {
+                float p[V];
+#pragma unroll
+                for (int v = 0; v < V; ++v) p[v] = product[NA == 1 ? 0 : v];
+                Some<float, V>::store(a.sum_a + q.slot * a.d + ch.c, p, ch.skip);
+                Some<float, V>::store(a.sum_b + q.slot * a.d + ch.c, s, ch.skip);
+            } else if (phase == kScanWhole) {
+                float* const last = BACK ? a.dh0 : a.h_last;
+                if (last) Some<float, V>::store(last + q.seq * a.d + ch.c, s, ch.skip);
+            }
+        }
+    }
+}
+
+// Whole sequences, or chunks' sums, the states between them, and the chunks.
+template <class TA, class T, int V, bool GROUPED, bool BACK>
+void run_scan(const ScanArgs& a, hipStream_t s) {
+    const bool split = a.p.chunk != 0;
+    const int64_t units = (split ? a.p.slots : a.n_seq) * a.p.blocks;
+    auto go = [&](auto waves, auto steps, int phase) {
+        constexpr int W = decltype(waves)::value, S = decltype(steps)::value;
+        const int64_t blocks = W == 1 ? (units + 3) / 4 : units;
+        k_scan<TA, T, V, GROUPED, W, S, BACK><<<(unsigned)(blocks < kScanGrid ? blocks : kScanGrid),
+                                                W == 1 ? 256 : 64 * W, 0, s>>>(a, units, phase);
+    };
+    using std::integral_constant;
+    auto phase = [&](int p) {
+        if (a.p.waves == 1 && !a.offsets && a.len <= 1)
+            go(integral_constant<int, 1>{}, integral_constant<int, 1>{}, p);
+        else if (a.p.waves == 1)
+            go(integral_constant<int, 1>{}, integral_constant<int, kSteps>{}, p);
+        else if (a.p.waves == 4)
+            go(integral_constant<int, 4>{}, integral_constant<int, kSteps>{}, p);
+        else
+            go(integral_constant<int, 8>{}, integral_constant<int, kSteps>{}, p);
+    };
+    if (!split) {
+        phase(kScanWhole);
+    } else {
+        phase(kScanSums);
+        launch_scan_carry(a, BACK ? a.dh_last : a.h0, BACK ? a.dh0 : a.h_last, s);
+        phase(kScanApply);
+    }
+}
+
+template <class TA, class T, bool BACK>
+void pick_scan(const ScanArgs& a, hipStream_t s) {
+    constexpr int V = 8 / (int)sizeof(T);
+    if (a.p.grouped) {
+        if (a.p.vec)
+            run_scan<TA, T, V, true, BACK>(a, s);
+        else
+            run_scan<TA, T, 1, true, BACK>(a, s);
+    } else {
+        if (a.p.vec)
+            run_scan<TA, T, V, false, BACK>(a, s);
+        else
+            run_scan<TA, T, 1, false, BACK>(a, s);
+    }
+}
+
+}  // namespace
+
+}  // namespace nerf
