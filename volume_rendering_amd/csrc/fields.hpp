@@ -90,6 +90,7 @@ struct ScanArgs {
     float* sum_a;              // split: [slots, d] products of a chunk's gates, then its state before
     float* sum_b;              // split: [slots, d] states of a chunk that began with 0
     float* part_da;            // [parts, rows, gates]
+    int near;                  // a wave's tile spans less than 2^32 bytes of every operand
     ScanPlan p;
 };
 ScanPlan scan_plan(int elt, int64_t rows, int64_t n_seq, int d, int gates);

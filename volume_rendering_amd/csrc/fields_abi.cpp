@@ -70,6 +70,9 @@ ScanArgs scan_args(const nerf_scan_cfg* c, const void* a, const void* x, const f
     s.h0 = h0;
     s.ld_h = c->ld_h ? c->ld_h : c->d;
     s.ld_dh = c->ld_dh ? c->ld_dh : c->d;
+    // (512 steps at most, of 4 bytes an element)
+    const int64_t far = (int64_t)1 << 20;
+    s.near = s.ld_a <= far && s.ld_x <= far && s.ld_h <= far && s.ld_dh <= far;
     s.p = scan_plan(elt_bytes(c->dtype), c->rows, c->n_seq, c->d, c->gates);
     return s;
 }

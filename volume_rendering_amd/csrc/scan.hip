@@ -88,7 +88,7 @@ ScanPlan scan_plan(int elt, int64_t rows, int64_t n_seq, int d, int gates) {
     }
     const int64_t run = (int64_t)(64 / p.cl) * 8;  // steps of one wave's tile
     const int64_t average = n_seq > 0 ? (rows + n_seq - 1) / n_seq : 0, units = n_seq * p.blocks;
-    p.waves = units >= 4096 || average <= run ? 1 : units >= 1024 || average <= 4 * run ? 4 : 8;
+    p.waves = units >= 16384 || average <= run ? 1 : units >= 1024 || average <= 4 * run ? 4 : 8;
     if (units < 256 && average > 32 * run) {
         p.waves = 4;
         const int64_t each = (2048 + units - 1) / units, tile = 4 * run;  // chunks of a sequence

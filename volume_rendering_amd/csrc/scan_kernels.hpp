@@ -136,7 +136,7 @@ __device__ __forceinline__ bool scan_unit(const ScanArgs& a, int64_t u, bool aga
 // of V starts earlier); none of them if !live.
 struct ScanLane {
     int c, gate, skip;
-    bool live;
+    bool live, gate_live;  // gate_live: the lane's gate exists
 };
 template <int V, bool GROUPED>
 __device__ __forceinline__ ScanLane scan_lane(const ScanArgs& a, int block, int cl) {
@@ -149,7 +149,8 @@ __device__ __forceinline__ ScanLane scan_lane(const ScanArgs& a, int block, int 
         r.live = r.gate < a.gates && want < m;
         const int c = want + V <= m ? want : m - V;
         r.skip = r.live ? want - c : V;
-        if (r.gate >= a.gates) r.gate = a.gates - 1;
+        r.gate_live = r.gate < a.gates;
+        if (!r.gate_live) r.gate = a.gates - 1;
         r.c = r.gate * m + c;
     } else {
         const int64_t want = ((int64_t)block * a.p.cl + cl) * V;
@@ -157,6 +158,7 @@ __device__ __forceinline__ ScanLane scan_lane(const ScanArgs& a, int block, int 
         r.c = want + V <= a.d ? (int)want : a.d - V;
         r.skip = r.live ? (int)want - r.c : V;
         r.gate = r.c;
+        r.gate_live = r.live;
     }
     return r;
 }
@@ -178,12 +180,28 @@ __device__ __forceinline__ Affine<NA, V> after(const Affine<NA, V>& first, const
 
 enum ScanPhase { kScanWhole = 0, kScanSums = 1, kScanApply = 2 };
 
-// Sums over lg lanes (a power of two) of kSteps values each; the lane's own
-// steps' sums are left in every lane.
-__device__ __forceinline__ void sum_over(float (&v)[kSteps], int lg) {
-    for (int off = lg / 2; off >= 1; off >>= 1)
+// Sums over lg lanes (a power of two) of kSteps values each.  While values are
+// left to halve, a lane keeps one half of them and hands over the other, so that
+// ten exchanges do for 64 lanes; lane g of the lg ends up with step
+// g / (lg / kSteps) (fewer lanes than steps: with steps from g kSteps / lg on).
+__device__ __forceinline__ void sum_over(float (&v)[kSteps], int lg, int lane) {
+    static_assert(kSteps == 8, "three halvings");
+    int off = lg / 2;
+    auto halve = [&](auto half) {
+        constexpr int H = decltype(half)::value;
+        if (off < 1) return;
+        const bool up = lane & off;
 #pragma unroll
-        for (int j = 0; j < kSteps; ++j) v[j] += __shfl_xor(v[j], off, 64);
+        for (int i = 0; i < H; ++i) {
+            const float give = up ? v[i] : v[i + H], keep = up ? v[i + H] : v[i];
+            v[i] = keep + __shfl_xor(give, off, 64);
+        }
+        off >>= 1;
+    };
+    halve(std::integral_constant<int, 4>{});
+    halve(std::integral_constant<int, 2>{});
+    halve(std::integral_constant<int, 1>{});
+    for (; off >= 1; off >>= 1) v[0] += __shfl_xor(v[0], off, 64);
 }
 
 // TA, T: types of the gates and of the rows; V channels a lane; W waves share a
@@ -196,14 +214,15 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W) k_scan(ScanArgs a, int6
     __shared__ Aff total[W == 1 ? 1 : 2][W][W == 1 ? 1 : 64];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int CL = a.p.cl, TL = 64 / CL, cl = lane % CL, tl = lane / CL;
-    const int64_t tile = (int64_t)W * TL * S;
+    const int run = TL * S;  // steps of a wave's tile
     const T* const in = (const T*)(BACK ? a.dh : a.x);
     const int64_t ld_in = BACK ? a.ld_dh : a.ld_x;
     int turn = 0;
     for (int64_t u = W == 1 ? (int64_t)blockIdx.x * 4 + wave : blockIdx.x; u < units;
          u += W == 1 ? (int64_t)gridDim.x * 4 : gridDim.x) {
         ScanUnit q;
-        if (!scan_unit(a, u, BACK, q)) continue;
+        // (chunks are applied in the opposite order of their sums: the last ones read are still in the caches)
+        if (!scan_unit(a, phase == kScanApply ? units - 1 - u : u, BACK, q)) continue;
         const ScanLane ch = scan_lane<V, GROUPED>(a, q.block, cl);
         // the state before the unit's first step
         float s[V];
@@ -226,89 +245,120 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W) k_scan(ScanArgs a, int6
 #pragma unroll
         for (int v = 0; v < NA; ++v) product[v] = 1.0f;
 
-        for (int64_t t0 = q.c0; t0 < q.c1; t0 += tile) {
-            const int64_t i0 = t0 + ((int64_t)(W == 1 ? 0 : wave) * TL + tl) * S;  // this lane's first step
-            const int64_t left = q.c1 - i0;                          // its steps: min(left, S), none if <= 0
-            // Loads of steps past the end repeat the last one's.
-            float ga[S][NA], gi[S][V];
-            auto row = [&](int j) {
-                const int64_t i = j < left ? i0 + j : q.c1 - 1;
-                return q.first + i * q.step;
-            };
+        for (int64_t t0 = q.c0; t0 < q.c1; t0 += (int64_t)W * run) {
+            const int64_t w0 = t0 + (W == 1 ? 0 : wave * run);  // the wave's first step
+            const int left = q.c1 - w0 < run ? (int)(q.c1 - w0) : run;  // its steps
+            const int mine = left - tl * S;                              // this lane's: min(mine, S)
+            const int64_t row0 = q.first + w0 * q.step;                  // row of the wave's first step
+            float ga[S][NA], gi[S][V], hp[BACK ? S : 1][V];
+            Aff lanes;  // the lane's run as one step
 #pragma unroll
-            for (int j = 0; j < S; ++j) {
-                const int64_t r = row(j);
-                Some<TA, NA>::load(ga[j], (const TA*)a.a + r * a.ld_a + ch.gate);
-                Some<T, V>::load(gi[j], in + r * ld_in + ch.c);
-            }
-            float hp[BACK ? S : 1][V], xs[BACK ? S : 1][V];
-            if constexpr (BACK) {
-                if (phase != kScanSums) {
+            for (int v = 0; v < NA; ++v) lanes.A[v] = 1.0f;
 #pragma unroll
-                    for (int j = 0; j < S; ++j) {
-                        const int64_t i = j < left ? i0 + j : q.c1 - 1, next = i + 1 < q.len ? i + 1 : i;
-                        Some<T, V>::load(hp[j], (const T*)a.h + (q.first + next * q.step) * a.ld_h + ch.c);
-                        if (i + 1 == q.len)
+            for (int v = 0; v < V; ++v) lanes.B[v] = 0.0f;
+
+            // Where every lane has all its steps (and the row after each) addresses are one
+            // offset a lane, the same for all steps, from bases that are the wave's; else steps
+            // past the end repeat the last one's loads and are left out.
+            auto fetch = [&](auto whole) {
+                constexpr bool WHOLE = decltype(whole)::value;
+                const int low = q.step > 0 ? 0 : run - S;  // lane offsets are not negative
+                const uint32_t lane_row = (uint32_t)(q.step > 0 ? tl * S : run - S - tl * S);
+                auto at = [&](auto* base, int64_t ld, int c, int j, int more) {
+                    using P = decltype(base);
+                    if constexpr (WHOLE) {
+                        P wave_base = base + (row0 - low + (int64_t)(j + more) * q.step) * ld;
+                        return (P)((const char*)wave_base + (lane_row * (uint32_t)ld + (uint32_t)c) * (uint32_t)sizeof(*base));
+                    } else {
+                        int i = tl * S + j;
+                        i = i < left ? i : left - 1;
+                        if (more && w0 + i + 1 < q.len) ++i;
+                        return base + (row0 + (int64_t)i * q.step) * ld + c;
+                    }
+                };
 #pragma unroll
-                            for (int v = 0; v < V; ++v) hp[j][v] = first_h[v];
+                for (int j = 0; j < S; ++j) {
+                    Some<TA, NA>::load(ga[j], at((const TA*)a.a, a.ld_a, ch.gate, j, 0));
+                    Some<T, V>::load(gi[j], at(in, ld_in, ch.c, j, 0));
+                }
+                if constexpr (BACK) {
+                    if (phase != kScanSums) {
+#pragma unroll
+                        for (int j = 0; j < S; ++j) Some<T, V>::load(hp[j], at((const T*)a.h, a.ld_h, ch.c, j, 1));
+                        if (!WHOLE)
+#pragma unroll
+                            for (int j = 0; j < S; ++j)
+                                if (w0 + tl * S + j + 1 == q.len)
+#pragma unroll
+                                    for (int v = 0; v < V; ++v) hp[j][v] = first_h[v];
                         if (a.mix) {
-                            Some<T, V>::load(xs[j], (const T*)a.x + (q.first + i * q.step) * a.ld_x + ch.c);
+                            float xs[S][V];
 #pragma unroll
-                            for (int v = 0; v < V; ++v) hp[j][v] -= xs[j][v];
+                            for (int j = 0; j < S; ++j) Some<T, V>::load(xs[j], at((const T*)a.x, a.ld_x, ch.c, j, 0));
+#pragma unroll
+                            for (int j = 0; j < S; ++j)
+#pragma unroll
+                                for (int v = 0; v < V; ++v) hp[j][v] -= xs[j][v];
                         }
                     }
+                } else if (a.mix) {
+#pragma unroll
+                    for (int j = 0; j < S; ++j)
+#pragma unroll
+                        for (int v = 0; v < V; ++v) gi[j][v] *= 1.0f - ga[j][NA == 1 ? 0 : v];
                 }
-            } else if (a.mix) {
 #pragma unroll
                 for (int j = 0; j < S; ++j)
+                    if (WHOLE || j < mine) {
 #pragma unroll
-                    for (int v = 0; v < V; ++v) gi[j][v] *= 1.0f - ga[j][NA == 1 ? 0 : v];
-            }
-            // the lane's run as one step
-            Aff run;
+                        for (int v = 0; v < V; ++v) {
+                            const float A = ga[j][NA == 1 ? 0 : v];
+                            lanes.B[v] = BACK ? A * (lanes.B[v] + gi[j][v]) : fmaf(A, lanes.B[v], gi[j][v]);
+                        }
 #pragma unroll
-            for (int v = 0; v < NA; ++v) run.A[v] = 1.0f;
-#pragma unroll
-            for (int v = 0; v < V; ++v) run.B[v] = 0.0f;
-#pragma unroll
-            for (int j = 0; j < S; ++j)
-                if (j < left) {
-#pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        const float A = ga[j][NA == 1 ? 0 : v];
-                        run.B[v] = BACK ? A * (run.B[v] + gi[j][v]) : fmaf(A, run.B[v], gi[j][v]);
+                        for (int v = 0; v < NA; ++v) lanes.A[v] *= ga[j][v];
                     }
-#pragma unroll
-                    for (int v = 0; v < NA; ++v) run.A[v] *= ga[j][v];
-                }
+            };
+            const bool whole = a.near && left == run && (!BACK || w0 + run < q.len);
+            if (whole)
+                fetch(std::true_type{});
+            else if (left > 0)
+                fetch(std::false_type{});
+
             // runs of the wave's lanes of the same channels, in order
-            for (int off = CL; off < 64; off <<= 1) {
-                Aff o;
+            Aff all = lanes, before;  // the wave's steps; those of the lanes before
 #pragma unroll
-                for (int v = 0; v < NA; ++v) o.A[v] = __shfl_up(run.A[v], off, 64);
+            for (int v = 0; v < NA; ++v) before.A[v] = 1.0f;
 #pragma unroll
-                for (int v = 0; v < V; ++v) o.B[v] = __shfl_up(run.B[v], off, 64);
-                if (lane >= off) run = after(o, run);
-            }
-            Aff all, before;  // the wave's steps; those of the lanes before
+            for (int v = 0; v < V; ++v) before.B[v] = 0.0f;
+            if (TL > 1) {
+                for (int off = CL; off < 64; off <<= 1) {
+                    Aff o;
 #pragma unroll
-            for (int v = 0; v < NA; ++v) {
-                all.A[v] = __shfl(run.A[v], 64 - CL + cl, 64);
-                const float A = __shfl_up(run.A[v], CL, 64);
-                before.A[v] = tl == 0 ? 1.0f : A;
-            }
+                    for (int v = 0; v < NA; ++v) o.A[v] = __shfl_up(lanes.A[v], off, 64);
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                all.B[v] = __shfl(run.B[v], 64 - CL + cl, 64);
-                const float B = __shfl_up(run.B[v], CL, 64);
-                before.B[v] = tl == 0 ? 0.0f : B;
+                    for (int v = 0; v < V; ++v) o.B[v] = __shfl_up(lanes.B[v], off, 64);
+                    if (lane >= off) lanes = after(o, lanes);
+                }
+#pragma unroll
+                for (int v = 0; v < NA; ++v) {
+                    all.A[v] = __shfl(lanes.A[v], 64 - CL + cl, 64);
+                    const float A = __shfl_up(lanes.A[v], CL, 64);
+                    if (tl > 0) before.A[v] = A;
+                }
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    all.B[v] = __shfl(lanes.B[v], 64 - CL + cl, 64);
+                    const float B = __shfl_up(lanes.B[v], CL, 64);
+                    if (tl > 0) before.B[v] = B;
+                }
             }
             // the state before the wave's first step, and after the tile
-            float mine[V];
+            float st[V];
             if constexpr (W == 1) {
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    mine[v] = s[v];
+                    st[v] = s[v];
                     s[v] = fmaf(all.A[NA == 1 ? 0 : v], s[v], all.B[v]);
                 }
                 if (phase == kScanSums)
@@ -323,7 +373,7 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W) k_scan(ScanArgs a, int6
                     const Aff o = total[turn][w][cl];
 #pragma unroll
                     for (int v = 0; v < V; ++v) {
-                        if (w == wave) mine[v] = s[v];
+                        if (w == wave) st[v] = s[v];
                         s[v] = fmaf(o.A[NA == 1 ? 0 : v], s[v], o.B[v]);
                     }
                     if (phase == kScanSums)
@@ -332,34 +382,36 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W) k_scan(ScanArgs a, int6
                 }
                 turn ^= 1;
             }
-            if (phase == kScanSums) continue;
+            if (phase == kScanSums || left <= 0) continue;
 #pragma unroll
-            for (int v = 0; v < V; ++v) mine[v] = fmaf(before.A[NA == 1 ? 0 : v], mine[v], before.B[v]);
+            for (int v = 0; v < V; ++v) st[v] = fmaf(before.A[NA == 1 ? 0 : v], st[v], before.B[v]);
             // the steps themselves
+            const int64_t lane0 = row0 + (int64_t)(tl * S) * q.step;
             if constexpr (!BACK) {
+                T* out = (T*)a.h + lane0 * a.ld_h + ch.c;
 #pragma unroll
-                for (int j = 0; j < S; ++j) {
+                for (int j = 0; j < S; ++j, out += q.step * a.ld_h) {
 #pragma unroll
-                    for (int v = 0; v < V; ++v) mine[v] = fmaf(ga[j][NA == 1 ? 0 : v], mine[v], gi[j][v]);
-                    if (j < left && ch.live)
-                        Some<T, V>::store((T*)a.h + (q.first + (i0 + j) * q.step) * a.ld_h + ch.c, mine, ch.skip);
+                    for (int v = 0; v < V; ++v) st[v] = fmaf(ga[j][NA == 1 ? 0 : v], st[v], gi[j][v]);
+                    if (j < mine && ch.live) Some<T, V>::store(out, st, ch.skip);
                 }
             } else {
                 float sum[kSteps];
+                T* out = (T*)a.dx + lane0 * a.d + ch.c;
+                TA* gate = (TA*)a.da + lane0 * a.gates + ch.c;
 #pragma unroll
-                for (int j = 0; j < S; ++j) {
-                    const int64_t r = q.first + (i0 + j) * q.step;
+                for (int j = 0; j < S; ++j, out += (int64_t)q.step * a.d, gate += (int64_t)q.step * a.gates) {
                     float dx[V], da[V];
 #pragma unroll
                     for (int v = 0; v < V; ++v) {
-                        const float A = ga[j][NA == 1 ? 0 : v], D = gi[j][v] + mine[v];
+                        const float A = ga[j][NA == 1 ? 0 : v], D = gi[j][v] + st[v];
                         dx[v] = a.mix ? (1.0f - A) * D : D;
                         da[v] = D * hp[j][v];
-                        mine[v] = A * D;
+                        st[v] = A * D;
                     }
-                    if (j < left && ch.live) {
-                        Some<T, V>::store((T*)a.dx + r * a.d + ch.c, dx, ch.skip);
-                        if constexpr (!GROUPED) Some<TA, V>::store((TA*)a.da + r * a.gates + ch.c, da, ch.skip);
+                    if (j < mine && ch.live) {
+                        Some<T, V>::store(out, dx, ch.skip);
+                        if constexpr (!GROUPED) Some<TA, V>::store(gate, da, ch.skip);
                     }
                     if constexpr (GROUPED) {
                         sum[j] = 0.0f;
@@ -370,17 +422,21 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W) k_scan(ScanArgs a, int6
                 if constexpr (GROUPED) {
 #pragma unroll
                     for (int j = S; j < kSteps; ++j) sum[j] = 0.0f;
-                    sum_over(sum, a.p.lg);
-                    if (ch.live && cl % a.p.lg == 0)
+                    const int lg = a.p.lg, g = cl % lg;
+                    sum_over(sum, lg, lane);
+                    const int have = lg >= kSteps ? 1 : kSteps / lg, each = lg >= kSteps ? lg / kSteps : 1;
+                    const bool owner = ch.gate_live;
+                    if (g % each == 0 && owner)
 #pragma unroll
-                        for (int j = 0; j < S; ++j)
-                            if (j < left) {
-                                const int64_t r = q.first + (i0 + j) * q.step;
-                                if (a.p.parts > 1)
-                                    a.part_da[((int64_t)(q.block % a.p.parts) * a.rows + r) * a.gates + ch.gate] = sum[j];
-                                else
-                                    ((TA*)a.da)[r * a.gates + ch.gate] = (TA)sum[j];
-                            }
+                        for (int i = 0; i < kSteps; ++i) {
+                            const int j = g / each * have + i;
+                            if (i >= have || j >= S || j >= mine) break;
+                            const int64_t r = lane0 + (int64_t)j * q.step;
+                            if (a.p.parts > 1)
+                                a.part_da[((int64_t)(q.block % a.p.parts) * a.rows + r) * a.gates + ch.gate] = sum[i];
+                            else
+                                ((TA*)a.da)[r * a.gates + ch.gate] = (TA)sum[i];
+                        }
                 }
             }
         }
