@@ -739,7 +739,7 @@ size_t nerf_scan_workspace_size(int64_t rows, int64_t n_seq, int d, int gates, i
  * sequence; it may be h0 (a stream's state, updated in place).  Errors: null
  * pointers, bad dtypes, sizes, strides or alignment, rows that are not n_seq
  * equal sequences, h == x or a, workspace too small; NERF_ERR_UNSUPPORTED for
- * bfloat16 gates of float32 rows. */
+ * bfloat16 gates of float32 rows and row strides above 2^26 elements. */
 nerf_status nerf_scan(const nerf_scan_cfg* cfg, const void* a, const void* x, const int32_t* offsets, const float* h0,
                       void* h, float* h_last, void* workspace, size_t workspace_bytes, void* stream);
 

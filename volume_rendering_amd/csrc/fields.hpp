@@ -90,10 +90,12 @@ struct ScanArgs {
     float* sum_a;              // split: [slots, d] products of a chunk's gates, then its state before
     float* sum_b;              // split: [slots, d] states of a chunk that began with 0
     float* part_da;            // [parts, rows, gates]
-    int near;                  // a wave's tile spans less than 2^32 bytes of every operand
     ScanPlan p;
 };
+// The strides decide the lanes alone, not the workspace.
 ScanPlan scan_plan(int elt, int64_t rows, int64_t n_seq, int d, int gates);
+void scan_plan_strides(ScanPlan& p, int64_t ld);
+constexpr int64_t kScanMaxLd = (int64_t)1 << 26;  // elements
 size_t scan_workspace(const ScanPlan& p, int64_t rows, int d, int gates, bool backward);
 // gate_bf16 implies bf16.
 void launch_scan(bool bf16, bool gate_bf16, const ScanArgs& a, hipStream_t s);

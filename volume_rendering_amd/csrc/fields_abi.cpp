@@ -50,6 +50,8 @@ nerf_status check_scan(const char* who, const nerf_scan_cfg* c, bool offsets, bo
     NERF_REQUIRE(!backward || c->ld_dh == 0 || c->ld_dh >= c->d, "%s: ld_dh %lld below d", who, (long long)c->ld_dh);
     if (c->gate_dtype == NERF_BF16 && c->dtype != NERF_BF16)
         return nerf_fail(NERF_ERR_UNSUPPORTED, "%s: bfloat16 gates of float32 rows", who);
+    if (std::max(std::max(c->ld_a, c->ld_x), std::max(c->ld_h, c->ld_dh)) > kScanMaxLd)
+        return nerf_fail(NERF_ERR_UNSUPPORTED, "%s: row strides above 2^26 elements", who);
     return NERF_OK;
 }
 
@@ -70,10 +72,8 @@ ScanArgs scan_args(const nerf_scan_cfg* c, const void* a, const void* x, const f
     s.h0 = h0;
     s.ld_h = c->ld_h ? c->ld_h : c->d;
     s.ld_dh = c->ld_dh ? c->ld_dh : c->d;
-    // (512 steps at most, of 4 bytes an element)
-    const int64_t far = (int64_t)1 << 20;
-    s.near = s.ld_a <= far && s.ld_x <= far && s.ld_h <= far && s.ld_dh <= far;
     s.p = scan_plan(elt_bytes(c->dtype), c->rows, c->n_seq, c->d, c->gates);
+    scan_plan_strides(s.p, std::max(std::max(s.ld_a, s.ld_x), std::max(s.ld_h, s.ld_dh)));
     return s;
 }
 

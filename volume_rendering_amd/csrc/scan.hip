@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(64 * kCarryWaves) k_scan_carry(ScanArgs a, con
 
 ScanPlan scan_plan(int elt, int64_t rows, int64_t n_seq, int d, int gates) {
     ScanPlan p{};
-    const int m = d / gates, wide = 8 / elt;
+    const int m = d / gates, wide = 4;
     p.grouped = gates < d;
     p.vec = (p.grouped ? m : d) >= wide;
     const int V = p.vec ? wide : 1;
@@ -96,6 +96,12 @@ ScanPlan scan_plan(int elt, int64_t rows, int64_t n_seq, int d, int gates) {
         p.slots = rows / p.chunk + n_seq;
     }
     return p;
+}
+
+// The steps of a wave's tile are within 32-bit byte offsets of each other: rows
+// far apart get all lanes for their channels, and so eight steps a tile.
+void scan_plan_strides(ScanPlan& p, int64_t ld) {
+    if ((64 / p.cl) * 8 * ld + 65536 > (int64_t)1 << 30) p.cl = 64;
 }
 
 size_t scan_workspace(const ScanPlan& p, int64_t rows, int d, int gates, bool backward) {

@@ -7,7 +7,7 @@
 // Both are recurrences s' = A s + B: the forward one with (a_t, b_t), the
 // gradient against the sequence with (a_t, a_t dh_t) on what flows into h_t
 // from behind.  n steps are again such a step, with the product of their A and
-// the state that they reach from 0; so a wave's lanes take runs of kSteps
+// the state that they reach from 0; so a wave's lanes take runs of S
 // consecutive steps each, join the runs by a scan of those pairs, and then walk
 // their own steps from the true state before them.  Products of gates only
 // carry states from run to run; within a run the recurrence itself is applied.
@@ -30,32 +30,56 @@ namespace nerf {
 
 namespace {
 
-constexpr int kSteps = 8;         // steps of a lane's run
 constexpr int kScanGrid = 1 << 20;
 
 // V consecutive elements at any element alignment (global memory takes wide
-// accesses at any address here).
+// accesses at any address here), held as the 32-bit words they are loaded in:
+// as elements the compiler gives each bfloat16 a register of its own.
 template <class T, int V>
 struct Some {
-    struct __attribute__((packed, aligned(sizeof(T)))) Raw {
+    static constexpr int WORDS = (V * (int)sizeof(T) + 3) / 4;
+    struct Raw {
+        uint32_t w[WORDS];
+    };
+    struct __attribute__((packed, aligned(sizeof(T)))) Memory {
         T e[V];
     };
-    static __device__ __forceinline__ void load(float (&f)[V], const T* p) {
-        const Raw r = *reinterpret_cast<const Raw*>(p);
+    static __device__ __forceinline__ Raw raw(const T* p) {
+        Raw r = {};
+        if constexpr (V * sizeof(T) % 4 == 0) {
+            struct __attribute__((packed, aligned(sizeof(T)))) Words {
+                uint32_t w[WORDS];
+            };
+            const Words m = *reinterpret_cast<const Words*>(p);
 #pragma unroll
-        for (int v = 0; v < V; ++v) f[v] = (float)r.e[v];
+            for (int i = 0; i < WORDS; ++i) r.w[i] = m.w[i];
+        } else {
+            r.w[0] = __builtin_bit_cast(uint16_t, p[0]);
+        }
+        return r;
+    }
+    static __device__ __forceinline__ float get(const Raw& r, int v) {
+        if constexpr (sizeof(T) == 4)
+            return __uint_as_float(r.w[v]);
+        else
+            return __uint_as_float((v & 1) ? r.w[v / 2] & 0xFFFF0000u : r.w[v / 2] << 16);
+    }
+    static __device__ __forceinline__ void load(float (&f)[V], const T* p) {
+        const Raw r = raw(p);
+#pragma unroll
+        for (int v = 0; v < V; ++v) f[v] = get(r, v);
     }
     // elements from `skip` on
     static __device__ __forceinline__ void store(T* p, const float (&f)[V], int skip) {
-        Raw r;
+        Memory m;
 #pragma unroll
-        for (int v = 0; v < V; ++v) r.e[v] = (T)f[v];
+        for (int v = 0; v < V; ++v) m.e[v] = (T)f[v];
         if (skip == 0) {
-            *reinterpret_cast<Raw*>(p) = r;
+            *reinterpret_cast<Memory*>(p) = m;
         } else {
 #pragma unroll
             for (int v = 0; v < V; ++v)
-                if (v >= skip) p[v] = r.e[v];
+                if (v >= skip) p[v] = m.e[v];
         }
     }
 };
@@ -180,15 +204,14 @@ __device__ __forceinline__ Affine<NA, V> after(const Affine<NA, V>& first, const
 
 enum ScanPhase { kScanWhole = 0, kScanSums = 1, kScanApply = 2 };
 
-// Sums over lg lanes (a power of two) of kSteps values each.  While values are
-// left to halve, a lane keeps one half of them and hands over the other, so that
-// ten exchanges do for 64 lanes; lane g of the lg ends up with step
-// g / (lg / kSteps) (fewer lanes than steps: with steps from g kSteps / lg on).
-__device__ __forceinline__ void sum_over(float (&v)[kSteps], int lg, int lane) {
-    static_assert(kSteps == 8, "three halvings");
-    int off = lg / 2;
-    auto halve = [&](auto half) {
-        constexpr int H = decltype(half)::value;
+// Sums over lg lanes (a power of two) of N values each, a power of two.  While
+// values are left to halve, a lane keeps one half of them and hands over the
+// other, so that ten exchanges do for eight values and 64 lanes; lane g of the
+// lg ends up with value g / (lg / N) (fewer lanes than values: with those from
+// g N / lg on).
+template <int H, int N>
+__device__ __forceinline__ void sum_halves(float (&v)[N], int off, int lane) {
+    if constexpr (H >= 1) {
         if (off < 1) return;
         const bool up = lane & off;
 #pragma unroll
@@ -196,16 +219,14 @@ __device__ __forceinline__ void sum_over(float (&v)[kSteps], int lg, int lane) {
             const float give = up ? v[i] : v[i + H], keep = up ? v[i + H] : v[i];
             v[i] = keep + __shfl_xor(give, off, 64);
         }
-        off >>= 1;
-    };
-    halve(std::integral_constant<int, 4>{});
-    halve(std::integral_constant<int, 2>{});
-    halve(std::integral_constant<int, 1>{});
-    for (; off >= 1; off >>= 1) v[0] += __shfl_xor(v[0], off, 64);
+        sum_halves<H / 2>(v, off / 2, lane);
+    } else {
+        for (; off >= 1; off >>= 1) v[0] += __shfl_xor(v[0], off, 64);
+    }
 }
 
 // TA, T: types of the gates and of the rows; V channels a lane; W waves share a
-// unit (1: each wave has its own); S steps a lane (kSteps, or 1 where sequences
+// unit (1: each wave has its own); S steps a lane (8 or 4, or 1 where sequences
 // are that short); BACK: the gradient.
 template <class TA, class T, int V, bool GROUPED, int W, int S, bool BACK>
 __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W) k_scan(ScanArgs a, int64_t units, int phase) {
@@ -250,76 +271,74 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W) k_scan(ScanArgs a, int6
             const int left = q.c1 - w0 < run ? (int)(q.c1 - w0) : run;  // its steps
             const int mine = left - tl * S;                              // this lane's: min(mine, S)
             const int64_t row0 = q.first + w0 * q.step;                  // row of the wave's first step
-            float ga[S][NA], gi[S][V], hp[BACK ? S : 1][V];
+            // (kept as loaded until they are used: bfloat16 rows take half the registers)
+            typename Some<TA, NA>::Raw ra[S];
+            typename Some<T, V>::Raw ri[S], rh[BACK ? S : 1], rx[BACK ? S : 1];
+            auto gate_of = [&](int j, int v) { return Some<TA, NA>::get(ra[j], NA == 1 ? 0 : v); };
+            auto in_of = [&](int j, int v) {
+                const float f = Some<T, V>::get(ri[j], v);
+                return !BACK && a.mix ? f * (1.0f - gate_of(j, v)) : f;
+            };
             Aff lanes;  // the lane's run as one step
 #pragma unroll
             for (int v = 0; v < NA; ++v) lanes.A[v] = 1.0f;
 #pragma unroll
             for (int v = 0; v < V; ++v) lanes.B[v] = 0.0f;
 
-            // Where every lane has all its steps (and the row after each) addresses are one
-            // offset a lane, the same for all steps, from bases that are the wave's; else steps
-            // past the end repeat the last one's loads and are left out.
+            // Addresses are 32-bit offsets of lanes from bases that are the wave's.  Where every
+            // lane has all its steps (and the row after each) a lane has one for all of them; else
+            // steps past the end repeat the last one's loads and are left out.
             auto fetch = [&](auto whole) {
                 constexpr bool WHOLE = decltype(whole)::value;
-                const int low = q.step > 0 ? 0 : run - S;  // lane offsets are not negative
-                const uint32_t lane_row = (uint32_t)(q.step > 0 ? tl * S : run - S - tl * S);
+                const bool up = q.step > 0;
+                // the lowest row that the wave reads, as offsets are not negative
+                const int64_t low = up ? row0 : row0 - (WHOLE ? run - S : left - 1);
+                const uint32_t lane_row = (uint32_t)(up ? tl * S : run - S - tl * S);
                 auto at = [&](auto* base, int64_t ld, int c, int j, int more) {
                     using P = decltype(base);
+                    int64_t row = low;
+                    uint32_t rel = lane_row;
                     if constexpr (WHOLE) {
-                        P wave_base = base + (row0 - low + (int64_t)(j + more) * q.step) * ld;
-                        return (P)((const char*)wave_base + (lane_row * (uint32_t)ld + (uint32_t)c) * (uint32_t)sizeof(*base));
+                        row += (int64_t)(j + more) * q.step;
                     } else {
                         int i = tl * S + j;
                         i = i < left ? i : left - 1;
-                        if (more && w0 + i + 1 < q.len) ++i;
-                        return base + (row0 + (int64_t)i * q.step) * ld + c;
+                        if (more) {
+                            if (w0 + i + 1 < q.len) ++i;
+                            row -= up ? 0 : 1;
+                        }
+                        rel = (uint32_t)(up ? i : left - 1 + more - i);
                     }
+                    return (P)((const char*)(base + row * ld) +
+                               (rel * (uint32_t)ld + (uint32_t)c) * (uint32_t)sizeof(*base));
                 };
 #pragma unroll
                 for (int j = 0; j < S; ++j) {
-                    Some<TA, NA>::load(ga[j], at((const TA*)a.a, a.ld_a, ch.gate, j, 0));
-                    Some<T, V>::load(gi[j], at(in, ld_in, ch.c, j, 0));
+                    ra[j] = Some<TA, NA>::raw(at((const TA*)a.a, a.ld_a, ch.gate, j, 0));
+                    ri[j] = Some<T, V>::raw(at(in, ld_in, ch.c, j, 0));
                 }
                 if constexpr (BACK) {
                     if (phase != kScanSums) {
 #pragma unroll
-                        for (int j = 0; j < S; ++j) Some<T, V>::load(hp[j], at((const T*)a.h, a.ld_h, ch.c, j, 1));
-                        if (!WHOLE)
+                        for (int j = 0; j < S; ++j) rh[j] = Some<T, V>::raw(at((const T*)a.h, a.ld_h, ch.c, j, 1));
+                        if (a.mix)
 #pragma unroll
-                            for (int j = 0; j < S; ++j)
-                                if (w0 + tl * S + j + 1 == q.len)
-#pragma unroll
-                                    for (int v = 0; v < V; ++v) hp[j][v] = first_h[v];
-                        if (a.mix) {
-                            float xs[S][V];
-#pragma unroll
-                            for (int j = 0; j < S; ++j) Some<T, V>::load(xs[j], at((const T*)a.x, a.ld_x, ch.c, j, 0));
-#pragma unroll
-                            for (int j = 0; j < S; ++j)
-#pragma unroll
-                                for (int v = 0; v < V; ++v) hp[j][v] -= xs[j][v];
-                        }
+                            for (int j = 0; j < S; ++j) rx[j] = Some<T, V>::raw(at((const T*)a.x, a.ld_x, ch.c, j, 0));
                     }
-                } else if (a.mix) {
-#pragma unroll
-                    for (int j = 0; j < S; ++j)
-#pragma unroll
-                        for (int v = 0; v < V; ++v) gi[j][v] *= 1.0f - ga[j][NA == 1 ? 0 : v];
                 }
 #pragma unroll
                 for (int j = 0; j < S; ++j)
                     if (WHOLE || j < mine) {
 #pragma unroll
                         for (int v = 0; v < V; ++v) {
-                            const float A = ga[j][NA == 1 ? 0 : v];
-                            lanes.B[v] = BACK ? A * (lanes.B[v] + gi[j][v]) : fmaf(A, lanes.B[v], gi[j][v]);
+                            const float A = gate_of(j, v), in = in_of(j, v);
+                            lanes.B[v] = BACK ? A * (lanes.B[v] + in) : fmaf(A, lanes.B[v], in);
                         }
 #pragma unroll
-                        for (int v = 0; v < NA; ++v) lanes.A[v] *= ga[j][v];
+                        for (int v = 0; v < NA; ++v) lanes.A[v] *= gate_of(j, v);
                     }
             };
-            const bool whole = a.near && left == run && (!BACK || w0 + run < q.len);
+            const bool whole = left == run && (!BACK || w0 + run < q.len);
             if (whole)
                 fetch(std::true_type{});
             else if (left > 0)
@@ -392,21 +411,24 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W) k_scan(ScanArgs a, int6
 #pragma unroll
                 for (int j = 0; j < S; ++j, out += q.step * a.ld_h) {
 #pragma unroll
-                    for (int v = 0; v < V; ++v) st[v] = fmaf(ga[j][NA == 1 ? 0 : v], st[v], gi[j][v]);
+                    for (int v = 0; v < V; ++v) st[v] = fmaf(gate_of(j, v), st[v], in_of(j, v));
                     if (j < mine && ch.live) Some<T, V>::store(out, st, ch.skip);
                 }
             } else {
-                float sum[kSteps];
+                float sum[S];
                 T* out = (T*)a.dx + lane0 * a.d + ch.c;
                 TA* gate = (TA*)a.da + lane0 * a.gates + ch.c;
 #pragma unroll
                 for (int j = 0; j < S; ++j, out += (int64_t)q.step * a.d, gate += (int64_t)q.step * a.gates) {
                     float dx[V], da[V];
+                    const bool begins = w0 + tl * S + j + 1 == q.len;  // the sequence's first step
 #pragma unroll
                     for (int v = 0; v < V; ++v) {
-                        const float A = ga[j][NA == 1 ? 0 : v], D = gi[j][v] + st[v];
+                        const float A = gate_of(j, v), D = in_of(j, v) + st[v];
+                        float before = begins ? first_h[v] : Some<T, V>::get(rh[j], v);
+                        if (a.mix) before -= Some<T, V>::get(rx[j], v);
                         dx[v] = a.mix ? (1.0f - A) * D : D;
-                        da[v] = D * hp[j][v];
+                        da[v] = D * before;
                         st[v] = A * D;
                     }
                     if (j < mine && ch.live) {
@@ -420,17 +442,15 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W) k_scan(ScanArgs a, int6
                     }
                 }
                 if constexpr (GROUPED) {
-#pragma unroll
-                    for (int j = S; j < kSteps; ++j) sum[j] = 0.0f;
                     const int lg = a.p.lg, g = cl % lg;
-                    sum_over(sum, lg, lane);
-                    const int have = lg >= kSteps ? 1 : kSteps / lg, each = lg >= kSteps ? lg / kSteps : 1;
+                    sum_halves<S / 2>(sum, lg / 2, lane);
+                    const int have = lg >= S ? 1 : S / lg, each = lg >= S ? lg / S : 1;
                     const bool owner = ch.gate_live;
                     if (g % each == 0 && owner)
 #pragma unroll
-                        for (int i = 0; i < kSteps; ++i) {
+                        for (int i = 0; i < S; ++i) {
                             const int j = g / each * have + i;
-                            if (i >= have || j >= S || j >= mine) break;
+                            if (i >= have || j >= mine) break;
                             const int64_t r = lane0 + (int64_t)j * q.step;
                             if (a.p.parts > 1)
                                 a.part_da[((int64_t)(q.block % a.p.parts) * a.rows + r) * a.gates + ch.gate] = sum[i];
@@ -468,6 +488,8 @@ void run_scan(const ScanArgs& a, hipStream_t s) {
                                                 W == 1 ? 256 : 64 * W, 0, s>>>(a, units, phase);
     };
     using std::integral_constant;
+    // (the gradient of float32 rows holds twice the registers a step)
+    constexpr int kSteps = BACK ? 4 : 8;
     auto phase = [&](int p) {
         if (a.p.waves == 1 && !a.offsets && a.len <= 1)
             go(integral_constant<int, 1>{}, integral_constant<int, 1>{}, p);
@@ -489,7 +511,7 @@ void run_scan(const ScanArgs& a, hipStream_t s) {
 
 template <class TA, class T, bool BACK>
 void pick_scan(const ScanArgs& a, hipStream_t s) {
-    constexpr int V = 8 / (int)sizeof(T);
+    constexpr int V = 4;
     if (a.p.grouped) {
         if (a.p.vec)
             run_scan<TA, T, V, true, BACK>(a, s);
