@@ -69,13 +69,24 @@ struct Some {
 #pragma unroll
         for (int v = 0; v < V; ++v) f[v] = get(r, v);
     }
-    // elements from `skip` on
+    // Elements from `skip` on.  STREAM: not to be read again soon, so that the
+    // caches are left to the inputs (65536 rays x 16 float32 channels 139 us with
+    // ordinary stores, 108 with these; the gradient of two sequences of 32768 x
+    // 1024, whose chunks are read twice, 266 and 241).
+    template <bool STREAM = false>
     static __device__ __forceinline__ void store(T* p, const float (&f)[V], int skip) {
         Memory m;
 #pragma unroll
         for (int v = 0; v < V; ++v) m.e[v] = (T)f[v];
         if (skip == 0) {
-            *reinterpret_cast<Memory*>(p) = m;
+            constexpr int BYTES = V * (int)sizeof(T);
+            if constexpr (STREAM && BYTES >= 8) {
+                typedef uint32_t Vec __attribute__((ext_vector_type(BYTES / 4)));
+                typedef uint32_t Loose __attribute__((ext_vector_type(BYTES / 4), aligned(sizeof(T))));
+                __builtin_nontemporal_store(__builtin_bit_cast(Vec, m), reinterpret_cast<Loose*>(p));
+            } else {
+                *reinterpret_cast<Memory*>(p) = m;
+            }
         } else {
 #pragma unroll
             for (int v = 0; v < V; ++v)
@@ -412,7 +423,7 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W) k_scan(ScanArgs a, int6
                 for (int j = 0; j < S; ++j, out += q.step * a.ld_h) {
 #pragma unroll
                     for (int v = 0; v < V; ++v) st[v] = fmaf(gate_of(j, v), st[v], in_of(j, v));
-                    if (j < mine && ch.live) Some<T, V>::store(out, st, ch.skip);
+                    if (j < mine && ch.live) Some<T, V>::template store<true>(out, st, ch.skip);
                 }
             } else {
                 float sum[S];
@@ -432,8 +443,8 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W) k_scan(ScanArgs a, int6
                         st[v] = A * D;
                     }
                     if (j < mine && ch.live) {
-                        Some<T, V>::store(out, dx, ch.skip);
-                        if constexpr (!GROUPED) Some<TA, V>::store(gate, da, ch.skip);
+                        Some<T, V>::template store<true>(out, dx, ch.skip);
+                        if constexpr (!GROUPED) Some<TA, V>::template store<true>(gate, da, ch.skip);
                     }
                     if constexpr (GROUPED) {
                         sum[j] = 0.0f;
