@@ -196,7 +196,9 @@ nerf_status nerf_route_gate_grad(const float* dweights, const void* logits, int 
 
 size_t nerf_routed_mlp_workspace_size(int64_t n, int k, int hidden) {
     if (n < 1 || k < 1 || n > NERF_FEW_PAIRS / k || hidden < 1 || hidden > kMaxWidth) return 0;
-    return (size_t)n * (size_t)k * (((size_t)hidden + 7) & ~(size_t)7) * sizeof(float);
+    const size_t values = (size_t)n * (size_t)k * (((size_t)hidden + 7) & ~(size_t)7);
+    // (many pairs: in three bfloat16 parts, and the sorted pairs)
+    return n * k > kMlpSelfSorted ? kMlpPlanBytes + values * 6 : values * sizeof(float);
 }
 
 nerf_status nerf_routed_mlp(const nerf_routed_layer* L, const void* x, const int32_t* ids, const float* weights,
@@ -249,7 +251,8 @@ nerf_status nerf_routed_mlp(const nerf_routed_layer* L, const void* x, const int
     const nerf_status st = ws.take(who, workspace, workspace_bytes,
                                    nerf_routed_mlp_workspace_size(n, L->k, L->hidden), stream);
     if (st != NERF_OK) return st;
-    a.h = static_cast<float*>(ws.p);
+    a.plan = ws.p;
+    a.h = reinterpret_cast<float*>(static_cast<char*>(ws.p) + (n * L->k > kMlpSelfSorted ? kMlpPlanBytes : 0));
     (void)hipGetLastError();
     launch_routed_mlp(L->dtype == NERF_BF16, a, as_stream(stream));
     return ws.release(who, check_launch(who), stream);
