@@ -692,7 +692,7 @@ typedef struct {
 } nerf_routed_layer;
 
 /* Device workspace of nerf_routed_mlp (0 if the sizes are invalid). */
-size_t nerf_routed_mlp_workspace_size(int64_t n, int k, int hidden);
+size_t nerf_routed_mlp_workspace_size(int64_t n, int k, int hidden, int d_out);
 
 /* A whole two-layer routed field for a few samples:
  *   out_t = sum_j weights_tj (W2_e act(W1_e x_t + b1_e) + b2_e),  e = ids_tj,
@@ -701,7 +701,7 @@ size_t nerf_routed_mlp_workspace_size(int64_t n, int k, int hidden);
  * ids: device int32 [n, k]; weights: device float32 [n, k] or NULL (all 1); w1:
  * device [n_experts, hidden, d_in] (gated: 2 hidden rows); w2: device
  * [n_experts, d_out, hidden]; b1, b2: device float32 [n_experts, rows] or NULL;
- * out: device [n, d_out].  Hidden values stay in float32.  workspace: device,
+ * out: device [n, d_out].  Hidden values keep float32's 24 bits.  workspace: device,
  * 16-byte aligned, at least nerf_routed_mlp_workspace_size bytes, or NULL
  * (allocated stream-ordered).  Errors: null pointers, bad dtype, act, sizes,
  * strides or alignment, workspace too small; NERF_ERR_UNSUPPORTED for more than

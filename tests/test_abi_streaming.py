@@ -63,11 +63,11 @@ def test_routed_mlp_refusals():
         a[i] = ODD
         assert f(_layer(), *a, None, 0, None) == 1, i
     assert f(_layer(), None, None, None, 0, None, None, None, None, None, None, 0, None) == 0
-    need = B.nerf_routed_mlp_workspace_size(4, 2, 8)
-    assert need == 4 * 2 * 8 * 4
+    need = B.nerf_routed_mlp_workspace_size(4, 2, 8, 5)
+    assert need >= 4 * 2 * (8 + 5) * 4
     assert f(_layer(), P, P, P, 4, P, P, P, P, Q, P, need - 1, None) == 3
     assert f(_layer(), P, P, P, 4, P, P, P, P, Q, C.c_void_p(264), need, None) == 1
-    for bad in ((0, 2, 8), (4, 0, 8), (257, 2, 8), (4, 2, 0), (1 << 40, 2, 8)):
+    for bad in ((0, 2, 8, 5), (4, 0, 8, 5), (257, 2, 8, 5), (4, 2, 0, 5), (4, 2, 8, 0), (1 << 40, 2, 8, 5)):
         assert B.nerf_routed_mlp_workspace_size(*bad) == 0
 
 

@@ -157,7 +157,7 @@ def test_repeats_streams_graphs_and_workspaces():
     g = np.random.default_rng(4)
     args = _case(torch, g, 9, 3, 20, 200, 300, 100, "gated", True, 0.1, 0)
     x = args[0]
-    size = v.nerf_routed_mlp_workspace_size(9, 3, 300)
+    size = v.nerf_routed_mlp_workspace_size(9, 3, 300, 100)
     guard = torch.full((size + 64,), 171, dtype=torch.uint8, device="cuda")
 
     def call(ws=None):

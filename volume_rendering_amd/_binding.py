@@ -159,7 +159,7 @@ def lib():
             "nerf_distill_topk_grad": (I, [P, I, I64, I64, I64, P, P, I, C.c_float, P, P, P, I64, P]),
             "nerf_route_gate": (I, [P, I, I64, I64, I, I, I, P, P, P]),
             "nerf_route_gate_grad": (I, [P, P, I, I64, I64, I, I, I, P, P, P, I64, P]),
-            "nerf_routed_mlp_workspace_size": (S, [I64, I, I]),
+            "nerf_routed_mlp_workspace_size": (S, [I64, I, I, I]),
             "nerf_routed_mlp": (I, [C.POINTER(nerf_routed_layer), P, P, P, I64, P, P, P, P, P, P, S, P]),
             "nerf_scan_workspace_size": (S, [I64, I64, I, I, I]),
             "nerf_scan": (I, [C.POINTER(nerf_scan_cfg), P, P, P, P, P, P, P, S, P]),
@@ -636,8 +636,8 @@ def nerf_route_gate_grad(dweights, logits, ids, weights, dlogits, renorm=True):
     _check(lib().nerf_route_gate_grad(*args, _stream_handle()), "nerf_route_gate_grad")
 
 
-def nerf_routed_mlp_workspace_size(n: int, k: int, hidden: int) -> int:
-    return lib().nerf_routed_mlp_workspace_size(n, k, hidden)
+def nerf_routed_mlp_workspace_size(n: int, k: int, hidden: int, d_out: int) -> int:
+    return lib().nerf_routed_mlp_workspace_size(n, k, hidden, d_out)
 
 
 def nerf_routed_mlp(x, ids, weights, w1, b1, w2, b2, out, act="relu", workspace=None):

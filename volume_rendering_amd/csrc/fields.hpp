@@ -50,13 +50,14 @@ struct MlpArgs {
     const float* b2;
     float* h;              // workspace [n k][ld_h], or three bfloat16 planes of that
     int64_t ld_h;
-    int64_t plane;         // elements of a plane (0: float32); the launcher's choice
+    int64_t plane;         // elements of a plane
+    float* y;              // workspace [n k][d_out]
     void* plan;            // workspace: the sorted pairs, above kMlpSelfSorted
     void* out;             // [n, d_out]
     int64_t ld_out;
 };
 constexpr int kMlpSelfSorted = 64;       // pairs that need no plan
-constexpr size_t kMlpPlanBytes = 16640;
+constexpr size_t kMlpPlanBytes = 16640;  // whole 256 bytes
 void launch_routed_mlp(bool bf16, const MlpArgs& a, hipStream_t s);
 
 // ---- gated linear recurrence (scan_kernels.hpp, scan.hip, scan_grad.hip) ----

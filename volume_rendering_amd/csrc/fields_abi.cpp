@@ -55,6 +55,9 @@ nerf_status check_scan(const char* who, const nerf_scan_cfg* c, bool offsets, bo
     return NERF_OK;
 }
 
+// Rows of the hidden values start at whole 16 bytes of either form.
+size_t hidden_bytes(size_t pairs, int hidden) { return pairs * (((size_t)hidden + 7) & ~(size_t)7) * 6; }
+
 ScanArgs scan_args(const nerf_scan_cfg* c, const void* a, const void* x, const float* h0, const int32_t* offsets) {
     ScanArgs s{};
     s.rows = c->rows;
@@ -194,11 +197,13 @@ nerf_status nerf_route_gate_grad(const float* dweights, const void* logits, int 
     return check_launch(who);
 }
 
-size_t nerf_routed_mlp_workspace_size(int64_t n, int k, int hidden) {
-    if (n < 1 || k < 1 || n > NERF_FEW_PAIRS / k || hidden < 1 || hidden > kMaxWidth) return 0;
-    const size_t values = (size_t)n * (size_t)k * (((size_t)hidden + 7) & ~(size_t)7);
-    // (many pairs: in three bfloat16 parts, and the sorted pairs)
-    return n * k > kMlpSelfSorted ? kMlpPlanBytes + values * 6 : values * sizeof(float);
+// The sorted pairs, the hidden values (float32, or three bfloat16 parts) and the
+// outputs per pair.
+size_t nerf_routed_mlp_workspace_size(int64_t n, int k, int hidden, int d_out) {
+    if (n < 1 || k < 1 || n > NERF_FEW_PAIRS / k || hidden < 1 || hidden > kMaxWidth || d_out < 1 || d_out > kMaxWidth)
+        return 0;
+    const size_t pairs = (size_t)n * (size_t)k;
+    return kMlpPlanBytes + hidden_bytes(pairs, hidden) + pairs * (size_t)d_out * sizeof(float);
 }
 
 nerf_status nerf_routed_mlp(const nerf_routed_layer* L, const void* x, const int32_t* ids, const float* weights,
@@ -249,10 +254,12 @@ nerf_status nerf_routed_mlp(const nerf_routed_layer* L, const void* x, const int
     a.ld_out = L->ld_out ? L->ld_out : L->d_out;
     Workspace ws;
     const nerf_status st = ws.take(who, workspace, workspace_bytes,
-                                   nerf_routed_mlp_workspace_size(n, L->k, L->hidden), stream);
+                                   nerf_routed_mlp_workspace_size(n, L->k, L->hidden, L->d_out), stream);
     if (st != NERF_OK) return st;
-    a.plan = ws.p;
-    a.h = reinterpret_cast<float*>(static_cast<char*>(ws.p) + (n * L->k > kMlpSelfSorted ? kMlpPlanBytes : 0));
+    char* const p = static_cast<char*>(ws.p);
+    a.plan = p;
+    a.h = reinterpret_cast<float*>(p + kMlpPlanBytes);
+    a.y = reinterpret_cast<float*>(p + kMlpPlanBytes + hidden_bytes((size_t)n * L->k, L->hidden));
     (void)hipGetLastError();
     launch_routed_mlp(L->dtype == NERF_BF16, a, as_stream(stream));
     return ws.release(who, check_launch(who), stream);
