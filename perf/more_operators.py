@@ -230,7 +230,7 @@ def prepare(case, seed):
         s["w2"], s["b2"] = normal(E, dout, hid, scale=math.sqrt(2.0 / hid), dtype=dt), normal(E, dout, scale=0.1)
         if own:
             s["out"] = empty(n, dout, dtype=dt)
-            s["ws"] = empty(max(1, v.nerf_routed_mlp_workspace_size(n, k, hid)), dtype=torch.uint8)
+            s["ws"] = empty(max(1, v.nerf_routed_mlp_workspace_size(n, k, hid, dout)), dtype=torch.uint8)
         return s
     if case["op"] == "scan":
         dt, da, d, g, n = _DT[case["dtype"]], _DT[case["gate_dtype"]], case["d"], case["gates"], case["n"]
