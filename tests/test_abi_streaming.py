@@ -158,7 +158,7 @@ def test_binding_refuses_wrong_tensors():
             (lambda: v.nerf_route_gate(z(4, 8), z(4, 2), z(4, 2)), "ids: dtype|not a device"),
             (lambda: v.nerf_route_gate(z(4, 8).half(), z(4, 2, dtype=i32), z(4, 2)), "float32 or bfloat16|not a device"),
             (lambda: v.nerf_route_gate(z(8), z(4, 2, dtype=i32), z(4, 2)), "dimensions"),
-            (lambda: v.nerf_route_gate_grad(z(4, 2), None, z(4, 3, dtype=i32), z(4, 3), z(4, 8)), "dweights: shape"),
+            (lambda: v.nerf_route_gate_grad(z(4, 2), None, z(4, 3, dtype=i32), z(4, 3), z(4, 8)), "shape|not a device"),
             (lambda: v.nerf_routed_mlp(z(2, 4), z(2, 1, dtype=i32), None, z(3, 5, 4), None, z(3, 6, 5), None, z(2, 6),
                                        act="tanh"), "act"),
             (lambda: v.nerf_routed_mlp(z(2, 4), z(2, 1, dtype=i32), None, z(5, 4), None, z(3, 6, 5), None, z(2, 6)),

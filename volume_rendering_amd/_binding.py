@@ -9,6 +9,7 @@ library raises instead of falling back to anything else.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import os
 import sys
 
@@ -598,13 +599,40 @@ def nerf_distill_topk_grad(logits, t_logits, t_ids, temperature, lse, grad, row_
 # Streaming routed fields
 # ----------------------------------------------------------------------------
 
-def _here(*tensors):
-    """Refuses tensors of another device than the current one, on whose
-    stream the call would run."""
-    now = _torch().cuda.current_device()
-    for t in tensors:
-        if t is not None and t.device.index != now:
-            raise NerfError(f"tensor on {t.device}, but the current device is cuda:{now}")
+def _device(t, what: str) -> int:
+    device = t.get_device()
+    if device < 0:
+        raise NerfError(f"{what}: not a device tensor")
+    return device
+
+
+def _on(t, what: str, dtype, shape, device: int, strided: bool = False) -> int:
+    """_tensor, refusing tensors of another device than the call's too."""
+    if t is None:
+        return 0
+    if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
+        return t.data_ptr()
+    p = _tensor(t, what, dtype, shape, strided)
+    if t.get_device() != device:
+        raise NerfError(f"{what}: on {t.device}, expected cuda:{device}")
+    return p
+
+
+def _ws_on(workspace, device: int):
+    p, n = _ws(workspace)
+    if workspace is not None and workspace.get_device() != device:
+        raise NerfError(f"workspace: on {workspace.device}, expected cuda:{device}")
+    return p, n
+
+
+def _stream_on(device: int) -> int:
+    """The current stream's handle; the tensors' device has to be the current
+    one, on whose stream the call runs."""
+    torch = _torch()
+    now = torch.cuda.current_device()
+    if now != device:
+        raise NerfError(f"tensors on cuda:{device}, but the current device is cuda:{now}")
+    return _stream_handle()
 
 
 def nerf_route_gate(logits, ids, weights, renorm=True):
@@ -615,10 +643,11 @@ def nerf_route_gate(logits, ids, weights, renorm=True):
     torch = _torch()
     n, E = _matrix(logits, "logits")
     k = _matrix(ids, "ids")[1]
-    args = (_tensor(logits, "logits", logits.dtype, (n, E), True), _dtype_of(logits, "logits"), _ld(logits), n, E, k,
-            int(renorm), _tensor(ids, "ids", torch.int32, (n, k)), _tensor(weights, "weights", torch.float32, (n, k)))
-    _here(logits, ids, weights)
-    _check(lib().nerf_route_gate(*args, _stream_handle()), "nerf_route_gate")
+    dev = _device(logits, "logits")
+    _check(lib().nerf_route_gate(_on(logits, "logits", logits.dtype, (n, E), dev, True), _dtype_of(logits, "logits"),
+                                 _ld(logits), n, E, k, int(renorm), _on(ids, "ids", torch.int32, (n, k), dev),
+                                 _on(weights, "weights", torch.float32, (n, k), dev), _stream_on(dev)),
+           "nerf_route_gate")
 
 
 def nerf_route_gate_grad(dweights, logits, ids, weights, dlogits, renorm=True):
@@ -628,16 +657,22 @@ def nerf_route_gate_grad(dweights, logits, ids, weights, dlogits, renorm=True):
     torch = _torch()
     n, E = _matrix(dlogits, "dlogits")
     k = _matrix(ids, "ids")[1]
-    dt, f32 = dlogits.dtype, torch.float32
-    args = (_tensor(dweights, "dweights", f32, (n, k)), _tensor(logits, "logits", dt, (n, E), True),
-            _dtype_of(dlogits, "dlogits"), _ld(logits), n, E, k, int(renorm), _tensor(ids, "ids", torch.int32, (n, k)),
-            _tensor(weights, "weights", f32, (n, k)), _tensor(dlogits, "dlogits", dt, (n, E), True), _ld(dlogits))
-    _here(dweights, logits, ids, weights, dlogits)
-    _check(lib().nerf_route_gate_grad(*args, _stream_handle()), "nerf_route_gate_grad")
+    dt, f32, dev = dlogits.dtype, torch.float32, _device(dlogits, "dlogits")
+    _check(lib().nerf_route_gate_grad(_on(dweights, "dweights", f32, (n, k), dev),
+                                      _on(logits, "logits", dt, (n, E), dev, True), _dtype_of(dlogits, "dlogits"),
+                                      _ld(logits), n, E, k, int(renorm), _on(ids, "ids", torch.int32, (n, k), dev),
+                                      _on(weights, "weights", f32, (n, k), dev),
+                                      _on(dlogits, "dlogits", dt, (n, E), dev, True), _ld(dlogits), _stream_on(dev)),
+           "nerf_route_gate_grad")
 
 
 def nerf_routed_mlp_workspace_size(n: int, k: int, hidden: int, d_out: int) -> int:
     return lib().nerf_routed_mlp_workspace_size(n, k, hidden, d_out)
+
+
+# The calls' configurations are plain values, and the same from call to call.
+_routed_layer = functools.lru_cache(maxsize=256)(lambda *values: nerf_routed_layer(*values))
+_scan_cfg = functools.lru_cache(maxsize=256)(lambda *values: nerf_scan_cfg(*values))
 
 
 def nerf_routed_mlp(x, ids, weights, w1, b1, w2, b2, out, act="relu", workspace=None):
@@ -656,32 +691,19 @@ def nerf_routed_mlp(x, ids, weights, w1, b1, w2, b2, out, act="relu", workspace=
     E, d_out, hidden = w2.shape
     (n, d_in), k = _matrix(x, "x"), _matrix(ids, "ids")[1]
     up = 2 * hidden if act == "gated" else hidden
-    dt, f32 = x.dtype, torch.float32
-    L = nerf_routed_layer(_dtype_of(x, "x"), E, d_in, hidden, d_out, _ACTS[act], k, _ld(x), _ld(out))
-    ws, wsb = _ws(workspace)
-    args = (_tensor(x, "x", dt, (n, d_in), True), _tensor(ids, "ids", torch.int32, (n, k)),
-            _tensor(weights, "weights", f32, (n, k)), n, _tensor(w1, "w1", dt, (E, up, d_in)),
-            _tensor(b1, "b1", f32, (E, up)), _tensor(w2, "w2", dt, (E, d_out, hidden)),
-            _tensor(b2, "b2", f32, (E, d_out)), _tensor(out, "out", dt, (n, d_out), True))
-    _here(x, ids, weights, w1, b1, w2, b2, out, workspace)
-    _check(lib().nerf_routed_mlp(C.byref(L), *args, ws, wsb, _stream_handle()), "nerf_routed_mlp")
+    dt, f32, dev = x.dtype, torch.float32, _device(x, "x")
+    L = _routed_layer(_dtype_of(x, "x"), E, d_in, hidden, d_out, _ACTS[act], k, _ld(x), _ld(out))
+    ws, wsb = _ws_on(workspace, dev)
+    _check(lib().nerf_routed_mlp(C.byref(L), _on(x, "x", dt, (n, d_in), dev, True),
+                                 _on(ids, "ids", torch.int32, (n, k), dev), _on(weights, "weights", f32, (n, k), dev),
+                                 n, _on(w1, "w1", dt, (E, up, d_in), dev), _on(b1, "b1", f32, (E, up), dev),
+                                 _on(w2, "w2", dt, (E, d_out, hidden), dev), _on(b2, "b2", f32, (E, d_out), dev),
+                                 _on(out, "out", dt, (n, d_out), dev, True), ws, wsb, _stream_on(dev)),
+           "nerf_routed_mlp")
 
 
 def nerf_scan_workspace_size(rows: int, d: int, gates=None, n_seq: int = 1, backward: bool = False) -> int:
     return lib().nerf_scan_workspace_size(rows, n_seq, d, d if gates is None else gates, int(backward))
-
-
-def _scan_cfg(a, x, offsets, n_seq, reverse, mix, ld_x, ld_h, ld_dh=0):
-    """The call's configuration from its gates and one [rows, d] tensor, and
-    the number of sequences."""
-    rows, d = _matrix(x, "x")
-    gates = _matrix(a, "a")[1]
-    if offsets is not None:
-        n_seq = offsets.numel() - 1
-    elif n_seq is None:
-        n_seq = 1
-    return nerf_scan_cfg(_dtype_of(x, "x"), _dtype_of(a, "a"), d, gates, int(reverse), int(mix), rows, n_seq, _ld(a),
-                         ld_x, ld_h, ld_dh), rows, d, gates, n_seq
 
 
 def nerf_scan(a, x, h, h0=None, h_last=None, offsets=None, n_seq=None, reverse=False, mix=False, workspace=None):
@@ -692,14 +714,16 @@ def nerf_scan(a, x, h, h0=None, h_last=None, offsets=None, n_seq=None, reverse=F
     ``reverse``: from the last row to the first.  ``h0`` float32 [n_seq, d] or
     None (0); ``h_last`` float32 [n_seq, d] or None, may be ``h0``."""
     torch = _torch()
-    cfg, rows, d, gates, n_seq = _scan_cfg(a, x, offsets, n_seq, reverse, mix, _ld(x), _ld(h))
-    f32 = torch.float32
-    ws, wsb = _ws(workspace)
-    args = (_tensor(a, "a", a.dtype, (rows, gates), True), _tensor(x, "x", x.dtype, (rows, d), True),
-            _tensor(offsets, "offsets", torch.int32, (n_seq + 1,)), _tensor(h0, "h0", f32, (n_seq, d)),
-            _tensor(h, "h", x.dtype, (rows, d), True), _tensor(h_last, "h_last", f32, (n_seq, d)))
-    _here(a, x, offsets, h0, h, h_last, workspace)
-    _check(lib().nerf_scan(C.byref(cfg), *args, ws, wsb, _stream_handle()), "nerf_scan")
+    (rows, d), gates = _matrix(x, "x"), _matrix(a, "a")[1]
+    n = offsets.numel() - 1 if offsets is not None else 1 if n_seq is None else n_seq
+    f32, dt, dev = torch.float32, x.dtype, _device(x, "x")
+    cfg = _scan_cfg(_dtype_of(x, "x"), _dtype_of(a, "a"), d, gates, int(reverse), int(mix), rows, n, _ld(a), _ld(x),
+                    _ld(h), 0)
+    ws, wsb = _ws_on(workspace, dev)
+    _check(lib().nerf_scan(C.byref(cfg), _on(a, "a", a.dtype, (rows, gates), dev, True),
+                           _on(x, "x", dt, (rows, d), dev, True), _on(offsets, "offsets", torch.int32, (n + 1,), dev),
+                           _on(h0, "h0", f32, (n, d), dev), _on(h, "h", dt, (rows, d), dev, True),
+                           _on(h_last, "h_last", f32, (n, d), dev), ws, wsb, _stream_on(dev)), "nerf_scan")
 
 
 def nerf_scan_grad(dh, a, x, h, da, dx, h0=None, dh_last=None, dh0=None, offsets=None, n_seq=None, reverse=False,
@@ -709,16 +733,19 @@ def nerf_scan_grad(dh, a, x, h, da, dx, h0=None, dh_last=None, dh0=None, offsets
     and ``dh0`` float32 [n_seq, d] or None (may be ``dh_last``).  ``h`` is the
     forward call's result; ``x`` may be None without ``mix``."""
     torch = _torch()
-    cfg, rows, d, gates, n_seq = _scan_cfg(a, dh, offsets, n_seq, reverse, mix, _ld(x), _ld(h), _ld(dh))
-    f32, dt = torch.float32, dh.dtype
-    ws, wsb = _ws(workspace)
-    args = (_tensor(dh, "dh", dt, (rows, d), True), _tensor(dh_last, "dh_last", f32, (n_seq, d)),
-            _tensor(a, "a", a.dtype, (rows, gates), True), _tensor(x, "x", dt, (rows, d), True),
-            _tensor(h, "h", dt, (rows, d), True), _tensor(h0, "h0", f32, (n_seq, d)),
-            _tensor(offsets, "offsets", torch.int32, (n_seq + 1,)), _tensor(da, "da", a.dtype, (rows, gates)),
-            _tensor(dx, "dx", dt, (rows, d)), _tensor(dh0, "dh0", f32, (n_seq, d)))
-    _here(dh, dh_last, a, x, h, h0, offsets, da, dx, dh0, workspace)
-    _check(lib().nerf_scan_grad(C.byref(cfg), *args, ws, wsb, _stream_handle()), "nerf_scan_grad")
+    (rows, d), gates = _matrix(dh, "dh"), _matrix(a, "a")[1]
+    n = offsets.numel() - 1 if offsets is not None else 1 if n_seq is None else n_seq
+    f32, dt, dev = torch.float32, dh.dtype, _device(dh, "dh")
+    cfg = _scan_cfg(_dtype_of(dh, "dh"), _dtype_of(a, "a"), d, gates, int(reverse), int(mix), rows, n, _ld(a), _ld(x),
+                    _ld(h), _ld(dh))
+    ws, wsb = _ws_on(workspace, dev)
+    _check(lib().nerf_scan_grad(C.byref(cfg), _on(dh, "dh", dt, (rows, d), dev, True),
+                                _on(dh_last, "dh_last", f32, (n, d), dev),
+                                _on(a, "a", a.dtype, (rows, gates), dev, True), _on(x, "x", dt, (rows, d), dev, True),
+                                _on(h, "h", dt, (rows, d), dev, True), _on(h0, "h0", f32, (n, d), dev),
+                                _on(offsets, "offsets", torch.int32, (n + 1,), dev),
+                                _on(da, "da", a.dtype, (rows, gates), dev), _on(dx, "dx", dt, (rows, d), dev),
+                                _on(dh0, "dh0", f32, (n, d), dev), ws, wsb, _stream_on(dev)), "nerf_scan_grad")
 
 
 class _TensorList:
@@ -754,25 +781,19 @@ def nerf_grad_norm_workspace_size(tensors) -> int:
 
 
 def _norm_args(tensors, norm, workspace):
-    torch = _torch()
-    ws, wsb = _ws(workspace)
-    p = _tensor(norm, "norm", torch.float32, (1,))
-    _here(norm, workspace)
-    if tensors.n and tensors.device != norm.device.index:
-        raise NerfError(f"tensors on cuda:{tensors.device}, but the current device is {norm.device}")
-    return p, ws, wsb
+    dev = _device(norm, "norm") if tensors.device is None else tensors.device
+    return (_on(norm, "norm", _torch().float32, (1,), dev), *_ws_on(workspace, dev), _stream_on(dev))
 
 
 def nerf_grad_norm(tensors, norm, workspace=None):
     """``norm`` (float32 [1]) of every element of every tensor of a
     nerf_tensor_list."""
-    p, ws, wsb = _norm_args(tensors, norm, workspace)
-    _check(lib().nerf_grad_norm(C.byref(tensors.array), tensors.n, p, ws, wsb, _stream_handle()), "nerf_grad_norm")
+    _check(lib().nerf_grad_norm(C.byref(tensors.array), tensors.n, *_norm_args(tensors, norm, workspace)),
+           "nerf_grad_norm")
 
 
 def nerf_grad_clip(tensors, max_norm: float, norm, workspace=None):
     """Scales every tensor of a nerf_tensor_list by min(1, max_norm / norm) into
     its output, and writes the ``norm`` from before (float32 [1])."""
-    p, ws, wsb = _norm_args(tensors, norm, workspace)
-    _check(lib().nerf_grad_clip(C.byref(tensors.array), tensors.n, float(max_norm), p, ws, wsb, _stream_handle()),
-           "nerf_grad_clip")
+    _check(lib().nerf_grad_clip(C.byref(tensors.array), tensors.n, float(max_norm),
+                                *_norm_args(tensors, norm, workspace)), "nerf_grad_clip")
