@@ -64,12 +64,40 @@ __device__ __forceinline__ float key_value(uint32_t key) {
     return key == ~0u ? __uint_as_float(0x7FC00000u) : __uint_as_float((key & 0x80000000u) ? key ^ 0x80000000u : ~key);
 }
 
+// The largest of G lanes' values, in each of them.  Up to 16 lanes exchange
+// within the vector units (pairs, fours, mirrored halves and rows of 16).
+template <int CONTROL>
+__device__ __forceinline__ uint32_t max_across(uint32_t v) {
+    const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CONTROL, 0xF, 0xF, true);
+    return o > v ? o : v;
+}
+template <int G>
+__device__ __forceinline__ uint32_t group_max(uint32_t v) {
+    if constexpr (G >= 2) v = max_across<0xB1>(v);    // lane ^ 1
+    if constexpr (G >= 4) v = max_across<0x4E>(v);    // lane ^ 2
+    if constexpr (G >= 8) v = max_across<0x141>(v);   // 7 - lane, of 8
+    if constexpr (G >= 16) v = max_across<0x140>(v);  // 15 - lane, of 16
+#pragma unroll
+    for (int off = 16; off < G; off <<= 1) {
+        const uint32_t o = __shfl_xor(v, off, 64);
+        v = o > v ? o : v;
+    }
+    return v;
+}
+
+// The rows' keys.  Those of bfloat16 logits have 16 bits and leave 12 for the
+// column, lowest first among equals, so that a maximum finds both.
+constexpr int kColumnBits = 12;
+static_assert(NERF_MAX_EXPERTS <= 1 << kColumnBits, "a column fits its key");
+constexpr uint32_t kLastColumn = (1u << kColumnBits) - 1;
+
 // Bound by instructions, not by memory: k rounds over the row's keys in
 // registers, each a maximum over the lane's own and log2 G exchanges.
 template <class T, int G, int NP>
 __global__ void __launch_bounds__(kGateThreads) k_gate(GateArgs a) {
     using Row = GateRow<T, G, NP>;
     constexpr int N = NP * Row::PER, ROWS = kGateThreads / G;
+    constexpr bool JOINT = sizeof(T) == 2;
     extern __shared__ char lds[];
     const int g = threadIdx.x % G, group = threadIdx.x / G;
     int* const ids = (int*)lds + group * a.k;
@@ -81,25 +109,33 @@ __global__ void __launch_bounds__(kGateThreads) k_gate(GateArgs a) {
         row.load((const T*)a.logits + r * a.ld, a.n_experts, g);
         uint32_t key[N];
 #pragma unroll
-        for (int i = 0; i < N; ++i) key[i] = order_key(row.z[i]);
+        for (int i = 0; i < N; ++i) {
+            key[i] = order_key(row.z[i]);
+            if constexpr (JOINT) key[i] = (key[i] >> 16) << kColumnBits | (kLastColumn - Row::column(g, i));
+        }
         float m = 0.0f, total = 0.0f;
         for (int j = 0; j < a.k; ++j) {
-            uint32_t best = 0;
+            uint32_t best = 0, mine = 0;
             int at = 0;
 #pragma unroll
             for (int i = 0; i < N; ++i)
-                if (key[i] > best) {
-                    best = key[i];
-                    at = Row::column(g, i);
+                if (key[i] > mine) {
+                    mine = key[i];
+                    if constexpr (!JOINT) at = Row::column(g, i);
                 }
+            best = group_max<G>(mine);
+            if constexpr (JOINT) {
+                at = (int)(kLastColumn - (best & kLastColumn));
 #pragma unroll
-            for (int off = G / 2; off >= 1; off >>= 1) {
-                const uint32_t o = __shfl_xor(best, off, 64);
-                const int oc = __shfl_xor(at, off, 64);
-                if (o > best || (o == best && oc < at)) {
-                    best = o;
-                    at = oc;
-                }
+                for (int i = 0; i < N; ++i) key[i] = key[i] == best ? 0u : key[i];
+                best = best >> kColumnBits << 16;
+                // (the bits that a float32 number has more: those of the numbers' complement are ones)
+                if (!(best & 0x80000000u) || best == 0xFFFF0000u) best |= 0xFFFFu;
+            } else {
+                at = (int)(kLastColumn - group_max<G>(mine == best ? kLastColumn - at : 0u));
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+                    if (Row::column(g, i) == at) key[i] = 0;
             }
             const bool some = best > kNoExpert;
             const float z = key_value(best);
@@ -112,9 +148,6 @@ __global__ void __launch_bounds__(kGateThreads) k_gate(GateArgs a) {
                 ids[j] = some ? at : -1;
                 zs[j] = some ? z : -INFINITY;
             }
-#pragma unroll
-            for (int i = 0; i < N; ++i)
-                if (Row::column(g, i) == at) key[i] = 0;
         }
         wave_lds_sync();
         if (r0 + group < a.n)
