@@ -194,6 +194,11 @@ def test_empty_calls_and_sequences():
                      offsets=off)
     assert torch.equal(d0, dl)
     v.nerf_scan(z, z, torch.empty_like(z), offsets=off[:1])  # no sequences
+    wide, gate = torch.empty((0, 600), device="cuda"), torch.empty((0, 1), device="cuda")  # a gate over several blocks
+    dl, d0 = torch.randn((3, 600), device="cuda"), torch.zeros((3, 600), device="cuda")
+    v.nerf_scan_grad(wide, gate, None, torch.empty_like(wide), torch.empty_like(gate), torch.empty_like(wide),
+                     dh_last=dl, dh0=d0, offsets=off)
+    assert torch.equal(d0, dl)
 
 
 @pytest.mark.parametrize("d", [8, 257, 1024])

@@ -28,7 +28,7 @@ ARCH = "gfx950"
 SOURCES = ["render_nerf_bf16.hip", "render_nerf_f32.hip", "render_hash.hip", "mlp_bf16.hip", "mlp_f32.hip",
            "kernels.hip", "kilo.hip", "abi.cpp", "pack.cpp", "layouts.cpp", "noalloc.hip", "train.hip", "hash_train.hip",
            "route.hip", "experts.hip", "distill.hip", "experts_abi.cpp", "gate.hip", "routed_mlp.hip", "scan.hip",
-           "scan_grad.hip", "clip.hip", "fields_abi.cpp"]
+           "scan_grad.hip", "scan_plan.cpp", "clip.hip", "fields_abi.cpp"]
 
 COMMON = ["-O3", "-std=c++17", "-fPIC", "-ffp-contract=off", f"-I{INCLUDE}", f"-I{CSRC}", "-Wall",
           "-Wno-unused-function"]

@@ -23,7 +23,7 @@ __global__ void __launch_bounds__(256) k_scan_gate_sums(ScanArgs a) {
 template <class TA, class T>
 void launch(const ScanArgs& a, hipStream_t s) {
     pick_scan<TA, T, true>(a, s);
-    if (a.p.parts > 1) {
+    if (a.p.parts > 1 && a.rows > 0) {
         const int64_t blocks = (a.rows * a.gates + 255) / 256;
         k_scan_gate_sums<TA><<<(unsigned)(blocks < kScanGrid ? blocks : kScanGrid), 256, 0, s>>>(a);
     }
