@@ -22,7 +22,7 @@ namespace nerf {
 
 namespace {
 
-constexpr int kGroup = 64;             // tensors a launch
+constexpr int kGroup = 128;            // tensors a launch (kernel arguments hold 4 KiB)
 constexpr int kClipThreads = 256;
 constexpr int kPiecesAhead = 8;        // 16-byte loads in flight per lane
 constexpr int kChunkPieces = kClipThreads * kPiecesAhead;  // 32 KiB
@@ -32,10 +32,11 @@ struct TensorGroup {
     const void* src[kGroup];
     void* dst[kGroup];
     int64_t count[kGroup];
-    int64_t first[kGroup + 1];  // chunks of the tensors before
-    uint64_t bf16;              // bit i: tensor i is bfloat16
+    int32_t first[kGroup + 1];  // chunks of the tensors before (fewer than 2^31: 2^41 elements at most)
+    uint32_t bf16[kGroup / 32]; // bit i: tensor i is bfloat16
     int n;
 };
+static_assert(sizeof(TensorGroup) + 32 <= 4096, "kernel arguments");
 
 __host__ __device__ inline int64_t chunks_of(int64_t count, bool bf16) {
     const int64_t per = (int64_t)kChunkPieces * (bf16 ? 8 : 4);
@@ -59,7 +60,7 @@ __device__ __forceinline__ Chunk chunk_at(const TensorGroup& g, int64_t c) {
     }
     Chunk r;
     r.t = lo;
-    r.bf16 = (g.bf16 >> lo) & 1;
+    r.bf16 = (g.bf16[lo / 32] >> lo % 32) & 1;
     const int64_t per = (int64_t)kChunkPieces * (r.bf16 ? 8 : 4);
     r.lo = (c - g.first[lo]) * per;
     r.hi = r.lo + per < g.count[lo] ? r.lo + per : g.count[lo];
@@ -188,7 +189,7 @@ __global__ void __launch_bounds__(kClipThreads) k_grad_scale(TensorGroup g, cons
 // next i.
 int next_group(TensorGroup& g, const nerf_tensor* list, int n, int i) {
     g.n = 0;
-    g.bf16 = 0;
+    for (uint32_t& bits : g.bf16) bits = 0;
     g.first[0] = 0;
     for (; i < n && g.n < kGroup; ++i) {
         if (list[i].count == 0) continue;
@@ -196,8 +197,8 @@ int next_group(TensorGroup& g, const nerf_tensor* list, int n, int i) {
         g.src[g.n] = list[i].src;
         g.dst[g.n] = list[i].dst;
         g.count[g.n] = list[i].count;
-        g.bf16 |= (uint64_t)bf16 << g.n;
-        g.first[g.n + 1] = g.first[g.n] + chunks_of(list[i].count, bf16);
+        g.bf16[g.n / 32] |= (uint32_t)bf16 << g.n % 32;
+        g.first[g.n + 1] = g.first[g.n] + (int32_t)chunks_of(list[i].count, bf16);
         ++g.n;
     }
     return i;

@@ -226,7 +226,8 @@ template <class T, int PARTS, int NG>
 __device__ __forceinline__ void matrix_dots(f32x4 (&acc)[NG], const T* w, const T* const (&x)[NG], int64_t plane,
                                             int64_t k0, int64_t k1, int lane) {
     using Vec = typename RowIO<T>::Vec;
-    constexpr int PER = RowIO<T>::PER, BK = 4 * PER, AHEAD = 4 / NG;
+    // loads in flight, as far as registers go
+    constexpr int PER = RowIO<T>::PER, BK = 4 * PER, AHEAD = PARTS == 1 ? (NG == 1 ? 6 : NG == 2 ? 4 : 3) : NG == 1 ? 4 : 2;
 #pragma unroll
     for (int n = 0; n < NG; ++n) acc[n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     for (int64_t kk = k0; kk < k1; kk += AHEAD * BK) {
@@ -278,9 +279,9 @@ __device__ __forceinline__ void by_sets(int count, F&& f) {
 
 // ---------------------------------------------------------------------------
 // Hidden layer by dot products.  A workgroup takes 16 rows of one expert's W1
-// (gated: 8 of either half) after the other, or 64 of rows that 16 lanes hold; G
-// lanes take kHidden rows (a wave of 1024-wide bfloat16 rows has eight weight loads
-// in flight per lane) and two pairs at once.
+// (gated: 8 of either half) after the other, more of rows that fewer than 64 lanes
+// hold; G lanes take kHidden rows (a wave of 1024-wide bfloat16 rows has eight
+// weight loads in flight per lane) and two pairs at once.
 // ---------------------------------------------------------------------------
 constexpr int kHiddenThreads = 256;
 constexpr int kHiddenGrid = 1024;
@@ -469,33 +470,33 @@ constexpr int kOutWaves = 8, kOutThreads = 64 * kOutWaves;
 constexpr int kPartFloats = 16 * NERF_FEW_PAIRS;  // of partial sums
 constexpr int kOutGroups = 256;
 
-template <class T, int OT, int M, class P>
+template <class T, int OT, int G, int M, class P>
 __device__ __forceinline__ void out_rows(const MlpArgs& a, const P& s, const T* const (&w)[OT], const float* bias, int at,
-                                         int64_t k0, int64_t k1, int lane, int first, float* part) {
+                                         int64_t k0, int64_t k1, int g, int first, float* part) {
     const float* x[M];
 #pragma unroll
     for (int m = 0; m < M; ++m) x[m] = a.h + (int64_t)(first + s.pair[at + m]) * a.ld_h;
-    const int i = lane / (64 / (OT * M));
+    const int i = g / (G / (OT * M));
     const float b = bias ? bias[i / M] : 0.0f;
     float acc[OT * M] = {};
-    dots<T, float, OT, M, 64>(acc, w, x, k0, k1, lane);
-    const float v = sum_lanes<OT * M, 64>(acc, lane) + b;
-    if (lane % (64 / (OT * M)) == 0) part[(at + i % M) * OT + i / M] = v;
+    dots<T, float, OT, M, G>(acc, w, x, k0, k1, g);
+    const float v = sum_lanes<OT * M, G>(acc, g) + b;
+    if (g % (G / (OT * M)) == 0) part[(at + i % M) * OT + i / M] = v;
 }
 
-template <class T, int OT, class P>
+template <class T, int OT, int G, class P>
 __device__ __forceinline__ void out_columns(const MlpArgs& a, const P& s, int64_t c0, int t0, int n, int room, float* part) {
-    constexpr int STEP = 64 * RowIO<T>::PER;
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    constexpr int STEP = G * RowIO<T>::PER, SUB = 64 / G, GROUPS = kOutWaves * SUB;
+    const int g = threadIdx.x % G, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int first = t0 * a.k, pairs = n * a.k;
     // fewer experts than waves: the waves share the hidden width too
     const int steps = (a.hidden + STEP - 1) / STEP;
-    int splits = s.experts > 0 && s.experts < kOutWaves ? kOutWaves / s.experts : 1;
+    int splits = s.experts > 0 && s.experts < GROUPS ? GROUPS / s.experts : 1;
     splits = splits < steps ? splits : steps;
     while (splits > 1 && splits * pairs * OT > room) --splits;
     const int64_t per = (int64_t)(steps + splits - 1) / splits * STEP;
     const bool all = c0 + OT <= a.d_out;  // (else the last column's bias is read for those past it)
-    for (int it = wave; it < s.experts * splits; it += kOutWaves) {
+    for (int it = wave * SUB + (SUB > 1 ? threadIdx.x % 64 / G : 0); it < s.experts * splits; it += GROUPS) {
         const int u = it / splits, ks = it % splits, e = s.expert[u];
         const T* w[OT];
 #pragma unroll
@@ -506,8 +507,8 @@ __device__ __forceinline__ void out_columns(const MlpArgs& a, const P& s, int64_
         const float* const bias = a.b2 && ks == 0 && all ? a.b2 + (int64_t)e * a.d_out + c0 : nullptr;
         int at = s.head[u];
         const int end = s.head[u + 1];
-        for (; at + 2 <= end; at += 2) out_rows<T, OT, 2>(a, s, w, bias, at, k0, k1, lane, first, mine);
-        if (at < end) out_rows<T, OT, 1>(a, s, w, bias, at, k0, k1, lane, first, mine);
+        for (; at + 2 <= end; at += 2) out_rows<T, OT, G, 2>(a, s, w, bias, at, k0, k1, g, first, mine);
+        if (at < end) out_rows<T, OT, G, 1>(a, s, w, bias, at, k0, k1, g, first, mine);
     }
     __syncthreads();
     for (int i = threadIdx.x; i < n * OT; i += kOutThreads) {
@@ -525,17 +526,17 @@ __device__ __forceinline__ void out_columns(const MlpArgs& a, const P& s, int64_
     }
 }
 
-template <class T, int OT, bool PLANNED>
+template <class T, int OT, int G, bool PLANNED>
 __global__ void __launch_bounds__(kOutThreads) k_mlp_out(MlpArgs a, int tiles, int samples, int room) {
     extern __shared__ float part[];  // `room` floats
     const int64_t c0 = (int64_t)(blockIdx.x % tiles) * OT;
     if constexpr (PLANNED) {
-        out_columns<T, OT>(a, *(const Plan*)a.plan, c0, 0, a.n, room, part);
+        out_columns<T, OT, G>(a, *(const Plan*)a.plan, c0, 0, a.n, room, part);
     } else {
         __shared__ __attribute__((aligned(16))) Pairs<kSelf> s;
         const int t0 = blockIdx.x / tiles * samples, n = t0 + samples < a.n ? samples : a.n - t0;
         sort_pairs(s, a, t0 * a.k, n * a.k, kOutThreads);
-        out_columns<T, OT>(a, s, c0, t0, n, room, part);
+        out_columns<T, OT, G>(a, s, c0, t0, n, room, part);
     }
 }
 
@@ -567,7 +568,7 @@ void launch_hidden(const MlpArgs& a, hipStream_t s) {
     });
 }
 
-template <class T, int OT>
+template <class T, int OT, int G = 64>
 void launch_out(const MlpArgs& a, hipStream_t s) {
     const int tiles = (a.d_out + OT - 1) / OT;
     // few columns: the samples are shared out too, until there is a workgroup for every CU
@@ -580,9 +581,9 @@ void launch_out(const MlpArgs& a, hipStream_t s) {
     const int all = samples * a.k * OT * kOutWaves, room = all < kPartFloats ? all : kPartFloats;
     const unsigned grid = (unsigned)(tiles * groups);
     if (planned)
-        k_mlp_out<T, OT, true><<<grid, kOutThreads, room * sizeof(float), s>>>(a, tiles, samples, room);
+        k_mlp_out<T, OT, G, true><<<grid, kOutThreads, room * sizeof(float), s>>>(a, tiles, samples, room);
     else
-        k_mlp_out<T, OT, false><<<grid, kOutThreads, room * sizeof(float), s>>>(a, tiles, samples, room);
+        k_mlp_out<T, OT, G, false><<<grid, kOutThreads, room * sizeof(float), s>>>(a, tiles, samples, room);
 }
 
 template <class T, bool FIRST, int SHARE>
@@ -616,13 +617,23 @@ void launch(MlpArgs a, hipStream_t s) {
         k_mlp_combine<T><<<(unsigned)(((int64_t)a.n * a.d_out + 255) / 256), 256, 0, s>>>(a);
         return;
     }
-    if (a.d_in <= 16 * RowIO<T>::PER)
+    // rows of few pieces take few lanes
+    const int in = (a.d_in + RowIO<T>::PER - 1) / RowIO<T>::PER, hidden = (a.hidden + RowIO<T>::PER - 1) / RowIO<T>::PER;
+    if (in <= 8)
+        launch_hidden<T, 8>(a, s);
+    else if (in <= 16)
         launch_hidden<T, 16>(a, s);
+    else if (in <= 32)
+        launch_hidden<T, 32>(a, s);
     else
         launch_hidden<T, 64>(a, s);
     // columns a workgroup: the more, the fewer reads of the hidden values; the fewer, the more workgroups (16
     // streams through 4 of 64 experts 1024 -> 1024: four 78 us, two 71; one sample through 4096 -> 1024: 11.6, 11.9)
-    if (a.d_out >= 4096)
+    if (hidden <= 16)
+        launch_out<T, 4, 16>(a, s);
+    else if (hidden <= 32)
+        launch_out<T, 4, 32>(a, s);
+    else if (a.d_out >= 4096)
         launch_out<T, 4>(a, s);
     else if (a.d_out >= 512)
         launch_out<T, 2>(a, s);
