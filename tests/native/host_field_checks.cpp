@@ -85,6 +85,7 @@ static void check_plan(const nerf::ScanArgs& a, bool backward) {
     ld = a.ld_h > ld ? a.ld_h : ld;
     if (backward && a.ld_dh > ld) ld = a.ld_dh;
     CHECK((64 / p.cl * 8 * ld + a.d) * 4 < (int64_t)1 << 32);
+    CHECK(!p.chunk || (!p.alone && a.n_seq < nerf::kScanMaxSplit));
     if (p.chunk) {
         CHECK(p.slots >= a.rows / p.chunk + a.n_seq && p.chunk % (p.waves * (64 / p.cl) * 4) == 0);
         std::memset(a.sum_a, 0, (size_t)p.slots * a.d * 4);
@@ -162,8 +163,8 @@ int main() {
     // recurrence: plans over its range
     for (int dt = 0; dt < 2; ++dt)
         for (int64_t rows : {0, 1, 7, 64, 1000, 5000, 200000})
-            for (int64_t n : {1, 2, 7, 300, 5000})
-                for (int d : {1, 2, 3, 4, 5, 16, 33, 63, 256, 257, 600, 1030})
+            for (int64_t n : {1, 2, 7, 16, 255, 300, 5000})
+                for (int d : {1, 2, 3, 4, 5, 16, 33, 63, 256, 257, 600, 1024, 1030})
                     for (int m : {1, 2, 3, 4, 5, 11, 33, 257, 515, 1030}) {
                         if (d % m) continue;
                         for (int64_t ld : {(int64_t)0, (int64_t)1 << 20, (int64_t)1 << 26}) {

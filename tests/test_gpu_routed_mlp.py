@@ -74,7 +74,12 @@ SIZES = [(1, 1, 1, 1, 1, 1, "relu", 0.0), (1, 2, 16, 96, 200, 64, "relu", 0.0), 
          (5, 3, 7, 17, 33, 9, "gated", 0.2), (64, 1, 300, 63, 32, 4, "relu", 0.3), (16, 4, 64, 128, 72, 40, "gated", 0.0),
          (8, 64, 3, 40, 24, 5, "relu", 0.1), (512, 1, 1, 24, 40, 33, "relu", 0.0), (100, 5, 2, 130, 65, 12, "gated", 0.1),
          (7, 2, 5, 1025, 519, 513, "relu", 0.0), (2, 2, 3, 256, 2049, 1031, "gated", 0.0), (4, 1, 9, 8, 7, 3, "none", 1.0),
-         (31, 3, 6, 3, 600, 2, "relu", 0.0), (2, 1, 2, 70, 1100, 1024, "none", 0.0)]
+         (31, 3, 6, 3, 600, 2, "relu", 0.0), (2, 1, 2, 70, 1100, 1024, "none", 0.0),
+         # rows of 24, 71 and 4100 weights, many columns, sorted pairs of few samples an expert
+         (9, 2, 70, 24, 71, 30, "gated", 0.1), (40, 3, 90, 71, 23, 200, "relu", 0.1), (3, 1, 4, 40, 16, 4103, "none", 0.0),
+         (2, 1, 3, 4100, 9, 6, "gated", 0.0), (150, 1, 100, 33, 20, 515, "gated", 0.2), (1, 5, 40, 16, 40, 1500, "relu", 0.0),
+         # 65 pairs and more an expert
+         (300, 1, 2, 40, 70, 64, "gated", 0.0), (256, 2, 3, 16, 130, 70, "relu", 0.2)]
 
 
 @pytest.mark.parametrize("pad", [0, 3])

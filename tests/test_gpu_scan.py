@@ -100,6 +100,11 @@ CASES = [
     ([6000, 0, 1, 3000], 70, 70, True, False),
     ([5000, 37], 130, 1, True, True),
     ([9001], 600, 2, False, True),
+    ([3, 0, 4, 2, 1, 4, 4, 3], 600, 1, True, True),      # walked alone, a gate over several blocks
+    ([1, 2, 0, 3, 4, 4, 4, 5], 24, 3, False, True),      # alone, gates side by side
+    ([4, 1, 0, 2], 1030, 1030, True, False),
+    ([120, 200, 0, 65, 64, 130], 256, 2, False, True),   # several tiles of eight waves
+    ([120, 200, 0, 65, 64, 128], 256, 256, True, True),
 ]
 
 
@@ -111,9 +116,38 @@ def _equal(lens):
 @pytest.mark.parametrize("dtype,gate_dtype", TYPES)
 @pytest.mark.parametrize("case", range(len(CASES)))
 def test_scan_and_gradient(case, dtype, gate_dtype, pad):
+    _check(case, CASES[case], dtype, gate_dtype, pad)
+
+
+def _ragged(n, top, seed):
+    return [int(v) for v in np.random.default_rng(seed).integers(0, top + 1, n)]
+
+
+# lengths, d, gates, reverse, mix, type, gates' type, pad
+LARGE = [
+    (_ragged(700, 24, 1), 256, 256, False, True, "bf16", "bf16", 0),   # many short ones: a lane's channels each
+    (_ragged(700, 24, 2), 256, 8, True, True, "f32", "f32", 3),
+    (_ragged(9000, 16, 3), 13, 1, False, False, "bf16", "f32", 0),
+    (_ragged(17000, 12, 4), 2, 2, True, True, "f32", "f32", 0),
+    ([40] * 8200, 4, 2, False, True, "bf16", "bf16", 1),               # rows of a few bytes
+    (_ragged(16, 280, 5), 1024, 1024, False, True, "bf16", "bf16", 0),  # fewer channels a workgroup
+    (_ragged(16, 280, 6), 1024, 16, True, False, "f32", "f32", 3),
+    (_ragged(20, 330, 7), 1026, 9, True, True, "bf16", "f32", 0),
+    (_ragged(70, 1400, 8), 64, 64, True, True, "bf16", "bf16", 0),      # chunks of more sequences than lanes
+    (_ragged(70, 330, 9), 256, 1, False, True, "f32", "f32", 0),
+]
+
+
+@pytest.mark.parametrize("case", range(len(LARGE)))
+def test_scan_and_gradient_of_many_sequences(case):
+    *shape, dtype, gate_dtype, pad = LARGE[case]
+    _check(100 + case, shape, dtype, gate_dtype, pad)
+
+
+def _check(case, shape, dtype, gate_dtype, pad):
     torch = torch_cuda()
     import volume_rendering_amd as v
-    lens, d, gates, reverse, mix = CASES[case]
+    lens, d, gates, reverse, mix = shape
     say(f"scan case={case} {dtype}/{gate_dtype} pad={pad} rows={sum(lens)} d={d} gates={gates}")
     g = np.random.default_rng([case, 1])
     behind = 5 if pad else 0  # rows behind the last sequence, left as they are
@@ -321,6 +355,41 @@ def test_repeats_streams_and_workspaces(rows, n, d, gates):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(p, q) for p, q in zip(held, call(None)))
+
+
+@pytest.mark.parametrize("d,gates", [(2, 2), (6, 1)])
+def test_rows_far_apart(d, gates):
+    """Rows so far apart that a wave's tile would leave 32-bit byte offsets."""
+    torch = torch_cuda()
+    import volume_rendering_amd as v
+    rows, ld = 21, (1 << 23) + 5
+    say(f"scan of rows {ld} apart, d={d} gates={gates}")
+    g = np.random.default_rng(d)
+    a, x, _ = _inputs(g, rows, d, gates, 1)
+    dh = g.standard_normal((rows, d))
+    def far(t, width):
+        big = torch.full(((rows - 1) * ld + width,), float("nan"), device="cuda").as_strided((rows, width), (ld, 1))
+        return big.copy_(torch.from_numpy(t.astype(np.float32)).cuda()) if t is not None else big
+    ta, tx, tdh = far(a, gates), far(x, d), far(dh, d)
+    th = far(np.zeros((rows, d)), d)
+    off = torch.tensor([0, 3, rows], dtype=torch.int32, device="cuda")
+    want = [torch.empty((rows, c), device="cuda") for c in (d, gates, d)]
+    near = [t.contiguous() for t in (ta, tx, tdh)]
+    for reverse in (False, True):
+        v.nerf_scan(ta, tx, th, offsets=off, reverse=reverse, mix=True)
+        v.nerf_scan(near[0], near[1], want[0], offsets=off, reverse=reverse, mix=True)
+        A, X = _f64(near[0]), _f64(near[1])
+        ref, _ = O.scan(A, X, [0, 3, rows], None, reverse, True)
+        _, E, _ = _bounds(A, (1 - np.repeat(A, d // gates, axis=1)) * X, [0, 3, rows], np.zeros((2, d)), reverse)
+        _close("h", _f64(th), ref, E + U * (np.abs(ref) + E))
+        da, dx = torch.empty((rows, gates), device="cuda"), torch.empty((rows, d), device="cuda")
+        v.nerf_scan_grad(tdh, ta, tx, th, da, dx, offsets=off, reverse=reverse, mix=True)
+        rda, rdx, _ = O.scan_grad(_f64(near[2]), None, A, X, _f64(th), None, [0, 3, rows], reverse, True)
+        # (21 terms of at most four roundings each, gates of at most 1: a bound of the magnitudes' sum)
+        m = np.abs(_f64(near[2])).sum(0)
+        assert (np.abs(_f64(dx) - rdx) <= 8 * rows * U * 2 * m).all()
+        top = np.abs(_f64(th)).max() + np.abs(X).max()
+        assert (np.abs(_f64(da) - rda) <= 8 * (rows + d) * U * m.sum() * top).all()
 
 
 def test_more_than_2_to_31_elements():

@@ -70,6 +70,8 @@ struct ScanPlan {
     int blocks;      // channel blocks: workgroups side by side
     int parts;       // channel blocks of one gate (partial sums of its gradient)
     int waves;       // waves that share a sequence (or chunk)
+    bool alone;      // a lane walks a sequence alone
+    bool stream;     // outputs are stored past the caches
     int64_t chunk;   // steps of a chunk, 0: sequences are not split
     int64_t slots;   // chunks at most
 };
@@ -100,6 +102,7 @@ struct ScanArgs {
 // The strides decide the lanes alone, not the workspace.
 ScanPlan scan_plan(int elt, int64_t rows, int64_t n_seq, int d, int gates);
 void scan_plan_strides(ScanPlan& p, int64_t ld);
+constexpr int kScanMaxSplit = 256;  // sequences of a call that is split
 constexpr int64_t kScanMaxLd = (int64_t)1 << 26;  // elements
 size_t scan_workspace(const ScanPlan& p, int64_t rows, int d, int gates, bool backward);
 // gate_bf16 implies bf16.

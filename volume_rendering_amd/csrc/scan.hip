@@ -22,7 +22,7 @@ __global__ void __launch_bounds__(64 * kCarryWaves) k_scan_carry(ScanArgs a, con
         const bool live = c < a.d;
         int64_t lo, len;
         sequence_rows(a, seq, lo, len);
-        const int64_t chunks = (len + a.p.chunk - 1) / a.p.chunk, slot = first_slot(a, seq);
+        const int64_t chunks = chunks_of(a, len), slot = first_slot(a, seq);
         const int64_t per = (chunks + kCarryWaves - 1) / kCarryWaves;
         const int64_t i0 = wave * per < chunks ? wave * per : chunks, i1 = i0 + per < chunks ? i0 + per : chunks;
         float A = 1.0f, B = 0.0f;

@@ -69,10 +69,7 @@ struct Some {
 #pragma unroll
         for (int v = 0; v < V; ++v) f[v] = get(r, v);
     }
-    // Elements from `skip` on.  STREAM: not to be read again soon, so that the
-    // caches are left to the inputs (65536 rays x 16 float32 channels 139 us with
-    // ordinary stores, 108 with these; the gradient of two sequences of 32768 x
-    // 1024, whose chunks are read twice, 266 and 241).
+    // Elements from `skip` on.  STREAM: past the caches, which are left to the inputs.
     template <bool STREAM = false>
     static __device__ __forceinline__ void store(T* p, const float (&f)[V], int skip) {
         Memory m;
@@ -84,9 +81,9 @@ struct Some {
                 typedef uint32_t Vec __attribute__((ext_vector_type(BYTES / 4)));
                 typedef uint32_t Loose __attribute__((ext_vector_type(BYTES / 4), aligned(sizeof(T))));
                 __builtin_nontemporal_store(__builtin_bit_cast(Vec, m), reinterpret_cast<Loose*>(p));
-            } else {
-                *reinterpret_cast<Memory*>(p) = m;
+                return;
             }
+            *reinterpret_cast<Memory*>(p) = m;
         } else {
 #pragma unroll
             for (int v = 0; v < V; ++v)
@@ -118,19 +115,35 @@ __device__ __forceinline__ void sequence_rows(const ScanArgs& a, int64_t seq, in
     }
 }
 
+// Quotient and remainder of numbers that mostly fit 32 bits.
+__device__ __forceinline__ int64_t quotient(int64_t u, int64_t by, int64_t& rest) {
+    if (((uint64_t)u | (uint64_t)by) >> 32) {
+        rest = u % by;
+        return u / by;
+    }
+    const uint32_t q = (uint32_t)u / (uint32_t)by;
+    rest = (uint32_t)u - q * (uint32_t)by;
+    return q;
+}
+
+// Chunks of a sequence of `len` steps (below 2^31).
+__device__ __forceinline__ int64_t chunks_of(const ScanArgs& a, int64_t len) {
+    return ((uint32_t)len + (uint32_t)a.p.chunk - 1) / (uint32_t)a.p.chunk;
+}
+
 // First chunk of a sequence: of equal ones their number each, else at most one
 // more than the whole chunks in front (room for every sequence's partial one).
 __device__ __forceinline__ int64_t first_slot(const ScanArgs& a, int64_t seq) {
-    if (!a.offsets) return seq * ((a.len + a.p.chunk - 1) / a.p.chunk);
-    return clamp_row(a.offsets[seq], a.rows) / a.p.chunk + seq;
+    if (!a.offsets) return seq * chunks_of(a, a.len);
+    return (uint32_t)clamp_row(a.offsets[seq], a.rows) / (uint32_t)a.p.chunk + seq;
 }
 
 // Unit `u` of a call that walks whole sequences (chunk 0), or of one chunk
-// each; false if there is nothing to do.
+// each; false if there is nothing to do.  By whole waves.
 __device__ __forceinline__ bool scan_unit(const ScanArgs& a, int64_t u, bool against, ScanUnit& r) {
-    int64_t lo;
-    r.block = (int)(u % a.p.blocks);
-    u /= a.p.blocks;
+    int64_t lo, rest = 0;
+    if (a.p.blocks > 1) u = quotient(u, a.p.blocks, rest);
+    r.block = (int)rest;
     r.slot = u;
     if (a.p.chunk == 0) {
         r.seq = u;
@@ -139,21 +152,20 @@ __device__ __forceinline__ bool scan_unit(const ScanArgs& a, int64_t u, bool aga
         r.c1 = r.len;
     } else {
         int64_t i;
-        if (a.offsets) {  // the last sequence whose first chunk is at or before u
-            int64_t s0 = 0, s1 = a.n_seq - 1;
-            while (s0 < s1) {
-                const int64_t mid = (s0 + s1 + 1) / 2;
-                if (first_slot(a, mid) <= u)
-                    s0 = mid;
-                else
-                    s1 = mid - 1;
+        if (a.offsets) {
+            // the last sequence whose first chunk is at or before u; there are few (kScanMaxSplit), so
+            // the lanes look at all of them at once
+            int before = 0;
+#pragma unroll
+            for (int j = 0; j < kScanMaxSplit / 64; ++j) {
+                const int64_t seq = 64 * j + lane_id();
+                before += __popcll(__ballot(seq < a.n_seq && first_slot(a, seq < a.n_seq ? seq : 0) <= u));
             }
-            r.seq = s0;
-            i = u - first_slot(a, s0);
+            r.seq = before - 1;
+            if (r.seq < 0) return false;
+            i = u - first_slot(a, r.seq);
         } else {
-            const int64_t per = (a.len + a.p.chunk - 1) / a.p.chunk;
-            r.seq = u / per;
-            i = u % per;
+            r.seq = quotient(u, chunks_of(a, a.len), i);
             if (r.seq >= a.n_seq) return false;
         }
         sequence_rows(a, r.seq, lo, r.len);
@@ -236,10 +248,31 @@ __device__ __forceinline__ void sum_halves(float (&v)[N], int off, int lane) {
     }
 }
 
+// The gradient of a lane's gate at S steps from row `first` on, of which it has
+// `mine`: the sum over the gate's lanes.
+template <class TA, int S>
+__device__ __forceinline__ void store_gate_sums(const ScanArgs& a, const ScanLane& ch, float (&sum)[S], int block, int cl,
+                                                int lane, int64_t first, int step, int mine) {
+    const int lg = a.p.lg, g = cl % lg;
+    sum_halves<S / 2>(sum, lg / 2, lane);
+    const int have = lg >= S ? 1 : S / lg, each = lg >= S ? lg / S : 1;
+    if (g % each != 0 || !ch.gate_live) return;
+#pragma unroll
+    for (int i = 0; i < S; ++i) {
+        const int j = g / each * have + i;
+        if (i >= have || j >= mine) break;
+        const int64_t r = first + (int64_t)j * step;
+        if (a.p.parts > 1)
+            a.part_da[((int64_t)(block % a.p.parts) * a.rows + r) * a.gates + ch.gate] = sum[i];
+        else
+            ((TA*)a.da)[r * a.gates + ch.gate] = (TA)sum[i];
+    }
+}
+
 // TA, T: types of the gates and of the rows; V channels a lane; W waves share a
-// unit (1: each wave has its own); S steps a lane (8 or 4, or 1 where sequences
-// are that short); BACK: the gradient.
-template <class TA, class T, int V, bool GROUPED, int W, int S, bool BACK>
+// unit (1: each wave has its own); S steps a lane; BACK: the gradient; STREAM:
+// outputs are stored past the caches.
+template <class TA, class T, int V, bool GROUPED, int W, int S, bool BACK, bool STREAM>
 __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W) k_scan(ScanArgs a, int64_t units, int phase) {
     constexpr int NA = GROUPED ? 1 : V;
     using Aff = Affine<NA, V>;
@@ -277,30 +310,27 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W) k_scan(ScanArgs a, int6
 #pragma unroll
         for (int v = 0; v < NA; ++v) product[v] = 1.0f;
 
-        for (int64_t t0 = q.c0; t0 < q.c1; t0 += (int64_t)W * run) {
-            const int64_t w0 = t0 + (W == 1 ? 0 : wave * run);  // the wave's first step
-            const int left = q.c1 - w0 < run ? (int)(q.c1 - w0) : run;  // its steps
-            const int mine = left - tl * S;                              // this lane's: min(mine, S)
-            const int64_t row0 = q.first + w0 * q.step;                  // row of the wave's first step
-            // (kept as loaded until they are used: bfloat16 rows take half the registers)
-            typename Some<TA, NA>::Raw ra[S];
-            typename Some<T, V>::Raw ri[S], rh[BACK ? S : 1], rx[BACK ? S : 1];
-            auto gate_of = [&](int j, int v) { return Some<TA, NA>::get(ra[j], NA == 1 ? 0 : v); };
-            auto in_of = [&](int j, int v) {
-                const float f = Some<T, V>::get(ri[j], v);
-                return !BACK && a.mix ? f * (1.0f - gate_of(j, v)) : f;
-            };
-            Aff lanes;  // the lane's run as one step
-#pragma unroll
-            for (int v = 0; v < NA; ++v) lanes.A[v] = 1.0f;
-#pragma unroll
-            for (int v = 0; v < V; ++v) lanes.B[v] = 0.0f;
-
-            // Addresses are 32-bit offsets of lanes from bases that are the wave's.  Where every
-            // lane has all its steps (and the row after each) a lane has one for all of them; else
-            // steps past the end repeat the last one's loads and are left out.
-            auto fetch = [&](auto whole) {
-                constexpr bool WHOLE = decltype(whole)::value;
+        // What a lane has loaded of a tile (kept as loaded until it is used: bfloat16 rows take half the registers).
+        struct Rows {
+            typename Some<TA, NA>::Raw a[S];
+            typename Some<T, V>::Raw in[S], h[BACK ? S : 1], x[BACK ? S : 1];
+        };
+        auto steps_of = [&](int64_t t0) {  // the wave's steps of a tile: at most `run`, none if <= 0
+            const int64_t w0 = t0 + (W == 1 ? 0 : wave * run);
+            return q.c1 - w0 < run ? (int)(q.c1 - w0) : run;
+        };
+        // Addresses are 32-bit offsets of lanes from bases that are the wave's.  Where every
+        // lane has all its steps (and the row after each) a lane has one for all of them; else
+        // steps past the end repeat the last one's loads and are left out.
+        auto whole_tile = [&](int64_t t0) {
+            const int64_t w0 = t0 + (W == 1 ? 0 : wave * run);
+            return steps_of(t0) == run && (!BACK || w0 + run < q.len);
+        };
+        auto fetch = [&](Rows& f, int64_t t0, auto whole) {
+            constexpr bool WHOLE = decltype(whole)::value;
+            const int64_t w0 = t0 + (W == 1 ? 0 : wave * run), row0 = q.first + w0 * q.step;
+            const int left = steps_of(t0);
+            {
                 const bool up = q.step > 0;
                 // the lowest row that the wave reads, as offsets are not negative
                 const int64_t low = up ? row0 : row0 - (WHOLE ? run - S : left - 1);
@@ -325,21 +355,51 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W) k_scan(ScanArgs a, int6
                 };
 #pragma unroll
                 for (int j = 0; j < S; ++j) {
-                    ra[j] = Some<TA, NA>::raw(at((const TA*)a.a, a.ld_a, ch.gate, j, 0));
-                    ri[j] = Some<T, V>::raw(at(in, ld_in, ch.c, j, 0));
+                    f.a[j] = Some<TA, NA>::raw(at((const TA*)a.a, a.ld_a, ch.gate, j, 0));
+                    f.in[j] = Some<T, V>::raw(at(in, ld_in, ch.c, j, 0));
                 }
                 if constexpr (BACK) {
                     if (phase != kScanSums) {
 #pragma unroll
-                        for (int j = 0; j < S; ++j) rh[j] = Some<T, V>::raw(at((const T*)a.h, a.ld_h, ch.c, j, 1));
+                        for (int j = 0; j < S; ++j) f.h[j] = Some<T, V>::raw(at((const T*)a.h, a.ld_h, ch.c, j, 1));
                         if (a.mix)
 #pragma unroll
-                            for (int j = 0; j < S; ++j) rx[j] = Some<T, V>::raw(at((const T*)a.x, a.ld_x, ch.c, j, 0));
+                            for (int j = 0; j < S; ++j) f.x[j] = Some<T, V>::raw(at((const T*)a.x, a.ld_x, ch.c, j, 0));
                     }
                 }
+            }
+        };
+
+        // With few workgroups (eight waves each) the next tile's loads are in flight while one is worked on.
+        constexpr bool AHEAD = W == 8;
+        Rows next;
+        auto fetch_next = [&](int64_t t0) {
+            if (whole_tile(t0))
+                fetch(next, t0, std::true_type{});
+            else if (steps_of(t0) > 0)
+                fetch(next, t0, std::false_type{});
+        };
+        if constexpr (AHEAD) fetch_next(q.c0);
+        for (int64_t t0 = q.c0; t0 < q.c1; t0 += (int64_t)W * run) {
+            const int64_t w0 = t0 + (W == 1 ? 0 : wave * run);  // the wave's first step
+            const int left = steps_of(t0);
+            const int mine = left - tl * S;              // this lane's steps: min(mine, S)
+            const int64_t row0 = q.first + w0 * q.step;  // row of the wave's first step
+            Rows f;
+            auto gate_of = [&](int j, int v) { return Some<TA, NA>::get(f.a[j], NA == 1 ? 0 : v); };
+            auto in_of = [&](int j, int v) {
+                const float in = Some<T, V>::get(f.in[j], v);
+                return !BACK && a.mix ? in * (1.0f - gate_of(j, v)) : in;
+            };
+            Aff lanes;  // the lane's run as one step
+#pragma unroll
+            for (int v = 0; v < NA; ++v) lanes.A[v] = 1.0f;
+#pragma unroll
+            for (int v = 0; v < V; ++v) lanes.B[v] = 0.0f;
+            auto fold = [&](auto whole) {
 #pragma unroll
                 for (int j = 0; j < S; ++j)
-                    if (WHOLE || j < mine) {
+                    if (decltype(whole)::value || j < mine) {
 #pragma unroll
                         for (int v = 0; v < V; ++v) {
                             const float A = gate_of(j, v), in = in_of(j, v);
@@ -349,11 +409,17 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W) k_scan(ScanArgs a, int6
                         for (int v = 0; v < NA; ++v) lanes.A[v] *= gate_of(j, v);
                     }
             };
-            const bool whole = left == run && (!BACK || w0 + run < q.len);
-            if (whole)
-                fetch(std::true_type{});
-            else if (left > 0)
-                fetch(std::false_type{});
+            if constexpr (AHEAD) {
+                f = next;
+                fetch_next(t0 + (int64_t)W * run);
+                fold(std::false_type{});
+            } else if (whole_tile(t0)) {
+                fetch(f, t0, std::true_type{});
+                fold(std::true_type{});
+            } else if (left > 0) {
+                fetch(f, t0, std::false_type{});
+                fold(std::false_type{});
+            }
 
             // runs of the wave's lanes of the same channels, in order
             Aff all = lanes, before;  // the wave's steps; those of the lanes before
@@ -423,7 +489,7 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W) k_scan(ScanArgs a, int6
                 for (int j = 0; j < S; ++j, out += q.step * a.ld_h) {
 #pragma unroll
                     for (int v = 0; v < V; ++v) st[v] = fmaf(gate_of(j, v), st[v], in_of(j, v));
-                    if (j < mine && ch.live) Some<T, V>::template store<true>(out, st, ch.skip);
+                    if (j < mine && ch.live) Some<T, V>::template store<STREAM>(out, st, ch.skip);
                 }
             } else {
                 float sum[S];
@@ -436,15 +502,15 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W) k_scan(ScanArgs a, int6
 #pragma unroll
                     for (int v = 0; v < V; ++v) {
                         const float A = gate_of(j, v), D = in_of(j, v) + st[v];
-                        float before = begins ? first_h[v] : Some<T, V>::get(rh[j], v);
-                        if (a.mix) before -= Some<T, V>::get(rx[j], v);
+                        float before = begins ? first_h[v] : Some<T, V>::get(f.h[j], v);
+                        if (a.mix) before -= Some<T, V>::get(f.x[j], v);
                         dx[v] = a.mix ? (1.0f - A) * D : D;
                         da[v] = D * before;
                         st[v] = A * D;
                     }
                     if (j < mine && ch.live) {
-                        Some<T, V>::template store<true>(out, dx, ch.skip);
-                        if constexpr (!GROUPED) Some<TA, V>::template store<true>(gate, da, ch.skip);
+                        Some<T, V>::template store<STREAM>(out, dx, ch.skip);
+                        if constexpr (!GROUPED) Some<TA, V>::template store<STREAM>(gate, da, ch.skip);
                     }
                     if constexpr (GROUPED) {
                         sum[j] = 0.0f;
@@ -452,23 +518,7 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W) k_scan(ScanArgs a, int6
                         for (int v = 0; v < V; ++v) sum[j] += ch.live && v >= ch.skip ? da[v] : 0.0f;
                     }
                 }
-                if constexpr (GROUPED) {
-                    const int lg = a.p.lg, g = cl % lg;
-                    sum_halves<S / 2>(sum, lg / 2, lane);
-                    const int have = lg >= S ? 1 : S / lg, each = lg >= S ? lg / S : 1;
-                    const bool owner = ch.gate_live;
-                    if (g % each == 0 && owner)
-#pragma unroll
-                        for (int i = 0; i < S; ++i) {
-                            const int j = g / each * have + i;
-                            if (i >= have || j >= mine) break;
-                            const int64_t r = lane0 + (int64_t)j * q.step;
-                            if (a.p.parts > 1)
-                                a.part_da[((int64_t)(q.block % a.p.parts) * a.rows + r) * a.gates + ch.gate] = sum[i];
-                            else
-                                ((TA*)a.da)[r * a.gates + ch.gate] = (TA)sum[i];
-                        }
-                }
+                if constexpr (GROUPED) store_gate_sums<TA, S>(a, ch, sum, q.block, cl, lane, lane0, q.step, mine);
             }
         }
         // (every wave has the state after the last tile)
@@ -487,29 +537,129 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W) k_scan(ScanArgs a, int6
     }
 }
 
+// Many sequences of few steps: a lane of a wave's 64 / CL time lanes has one of its
+// own, and walks it run by run; nothing is exchanged but the sums of a gate's
+// gradient.
+template <class TA, class T, int V, bool GROUPED, int S, bool BACK>
+__global__ void __launch_bounds__(256) k_scan_short(ScanArgs a, int64_t waves) {
+    constexpr int NA = GROUPED ? 1 : V;
+    const int lane = threadIdx.x & 63;
+    const int CL = a.p.cl, cl = lane % CL, each = 64 / CL;
+    const T* const in = (const T*)(BACK ? a.dh : a.x);
+    const int64_t ld_in = BACK ? a.ld_dh : a.ld_x;
+    for (int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); w < waves; w += (int64_t)gridDim.x * 4) {
+        int64_t block = 0;
+        const int64_t group = a.p.blocks > 1 ? quotient(w, a.p.blocks, block) : w;
+        const int64_t seq = group * each + lane / CL;
+        if (seq >= a.n_seq) continue;  // (its lanes leave together, and exchange only among themselves)
+        const ScanLane ch = scan_lane<V, GROUPED>(a, (int)block, cl);
+        int64_t lo, len;
+        sequence_rows(a, seq, lo, len);
+        const int step = (a.reverse != 0) != BACK ? -1 : 1;
+        const int64_t first = step > 0 ? lo : lo + len - 1;
+        float st[V], first_h[V];
+        const float* const from = BACK ? a.dh_last : a.h0;
+#pragma unroll
+        for (int v = 0; v < V; ++v) st[v] = first_h[v] = 0.0f;
+        if (from) Some<float, V>::load(st, from + seq * a.d + ch.c);
+        if (BACK && a.h0) Some<float, V>::load(first_h, a.h0 + seq * a.d + ch.c);
+        for (int64_t t0 = 0; t0 < len; t0 += S) {
+            const int left = len - t0 < S ? (int)(len - t0) : S;
+            typename Some<TA, NA>::Raw ra[S];
+            typename Some<T, V>::Raw ri[S], rh[BACK ? S : 1], rx[BACK ? S : 1];
+            // (steps past the end repeat the last one's loads)
+            auto row = [&](int j) { return first + (t0 + (j < left ? j : left - 1)) * step; };
+#pragma unroll
+            for (int j = 0; j < S; ++j) {
+                ra[j] = Some<TA, NA>::raw((const TA*)a.a + row(j) * a.ld_a + ch.gate);
+                ri[j] = Some<T, V>::raw(in + row(j) * ld_in + ch.c);
+            }
+            if constexpr (BACK) {
+#pragma unroll
+                for (int j = 0; j < S; ++j) {
+                    const int64_t r = row(j), before = t0 + (j < left ? j : left - 1) + 1 < len ? r + step : r;
+                    rh[j] = Some<T, V>::raw((const T*)a.h + before * a.ld_h + ch.c);
+                    if (a.mix) rx[j] = Some<T, V>::raw((const T*)a.x + r * a.ld_x + ch.c);
+                }
+            }
+            float sum[S];
+#pragma unroll
+            for (int j = 0; j < S; ++j) {
+                const bool has = j < left;
+                const int64_t r = first + (t0 + j) * step;
+                if constexpr (!BACK) {
+#pragma unroll
+                    for (int v = 0; v < V; ++v) {
+                        const float A = Some<TA, NA>::get(ra[j], NA == 1 ? 0 : v), x = Some<T, V>::get(ri[j], v);
+                        const float now = fmaf(A, st[v], a.mix ? x * (1.0f - A) : x);
+                        st[v] = has ? now : st[v];
+                    }
+                    if (has && ch.live) Some<T, V>::store((T*)a.h + r * a.ld_h + ch.c, st, ch.skip);
+                } else {
+                    float dx[V], da[V];
+                    const bool begins = t0 + j + 1 == len;
+#pragma unroll
+                    for (int v = 0; v < V; ++v) {
+                        const float A = Some<TA, NA>::get(ra[j], NA == 1 ? 0 : v), D = Some<T, V>::get(ri[j], v) + st[v];
+                        float before = begins ? first_h[v] : Some<T, V>::get(rh[j], v);
+                        if (a.mix) before -= Some<T, V>::get(rx[j], v);
+                        dx[v] = a.mix ? (1.0f - A) * D : D;
+                        da[v] = D * before;
+                        st[v] = has ? A * D : st[v];
+                    }
+                    if (has && ch.live) {
+                        Some<T, V>::store((T*)a.dx + r * a.d + ch.c, dx, ch.skip);
+                        if constexpr (!GROUPED)
+                            Some<TA, V>::store((TA*)a.da + r * a.gates + ch.c, da, ch.skip);
+                    }
+                    sum[j] = 0.0f;
+#pragma unroll
+                    for (int v = 0; v < V; ++v) sum[j] += ch.live && v >= ch.skip ? da[v] : 0.0f;
+                }
+            }
+            if constexpr (BACK && GROUPED) store_gate_sums<TA, S>(a, ch, sum, (int)block, cl, lane, first + t0 * step, step, left);
+        }
+        float* const last = BACK ? a.dh0 : a.h_last;
+        if (last && ch.live) Some<float, V>::store(last + seq * a.d + ch.c, st, ch.skip);
+    }
+}
+
 // Whole sequences, or chunks' sums, the states between them, and the chunks.
 template <class TA, class T, int V, bool GROUPED, bool BACK>
 void run_scan(const ScanArgs& a, hipStream_t s) {
     const bool split = a.p.chunk != 0;
     const int64_t units = (split ? a.p.slots : a.n_seq) * a.p.blocks;
-    auto go = [&](auto waves, auto steps, int phase) {
-        constexpr int W = decltype(waves)::value, S = decltype(steps)::value;
-        const int64_t blocks = W == 1 ? (units + 3) / 4 : units;
-        k_scan<TA, T, V, GROUPED, W, S, BACK><<<(unsigned)(blocks < kScanGrid ? blocks : kScanGrid),
-                                                W == 1 ? 256 : 64 * W, 0, s>>>(a, units, phase);
-    };
     using std::integral_constant;
     // (the gradient of float32 rows holds twice the registers a step)
     constexpr int kSteps = BACK ? 4 : 8;
-    auto phase = [&](int p) {
-        if (a.p.waves == 1 && !a.offsets && a.len <= 1)
-            go(integral_constant<int, 1>{}, integral_constant<int, 1>{}, p);
-        else if (a.p.waves == 1)
-            go(integral_constant<int, 1>{}, integral_constant<int, kSteps>{}, p);
-        else if (a.p.waves == 4)
-            go(integral_constant<int, 4>{}, integral_constant<int, kSteps>{}, p);
+    if (a.p.alone) {
+        const int64_t each = 64 / a.p.cl, waves = (a.n_seq + each - 1) / each * a.p.blocks, blocks = (waves + 3) / 4;
+        const unsigned grid = (unsigned)(blocks < kScanGrid ? blocks : kScanGrid);
+        if (!a.offsets && a.len <= 1)
+            k_scan_short<TA, T, V, GROUPED, 1, BACK><<<grid, 256, 0, s>>>(a, waves);
         else
-            go(integral_constant<int, 8>{}, integral_constant<int, kSteps>{}, p);
+            k_scan_short<TA, T, V, GROUPED, kSteps, BACK><<<grid, 256, 0, s>>>(a, waves);
+        return;
+    }
+    auto go = [&](auto waves, int phase) {
+        constexpr int W = decltype(waves)::value;
+        const int64_t blocks = W == 1 ? (units + 3) / 4 : units;
+        const unsigned grid = (unsigned)(blocks < kScanGrid ? blocks : kScanGrid), threads = W == 1 ? 256 : 64 * W;
+        if constexpr (V > 1) {
+            if (a.p.stream) {
+                k_scan<TA, T, V, GROUPED, W, kSteps, BACK, true><<<grid, threads, 0, s>>>(a, units, phase);
+                return;
+            }
+        }
+        k_scan<TA, T, V, GROUPED, W, kSteps, BACK, false><<<grid, threads, 0, s>>>(a, units, phase);
+    };
+    auto phase = [&](int p) {
+        if (a.p.waves == 1)
+            go(integral_constant<int, 1>{}, p);
+        else if (a.p.waves == 4)
+            go(integral_constant<int, 4>{}, p);
+        else
+            go(integral_constant<int, 8>{}, p);
     };
     if (!split) {
         phase(kScanWhole);

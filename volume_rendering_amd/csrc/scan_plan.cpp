@@ -39,12 +39,37 @@ ScanPlan scan_plan(int elt, int64_t rows, int64_t n_seq, int d, int gates) {
             p.blocks = gates * p.parts;
         }
     }
-    const int64_t run = (int64_t)(64 / p.cl) * 8;  // steps of one wave's tile
-    const int64_t average = n_seq > 0 ? (rows + n_seq - 1) / n_seq : 0, units = n_seq * p.blocks;
-    p.waves = units >= 16384 || average <= run ? 1 : units >= 1024 || average <= 4 * run ? 4 : 8;
-    if (units < 256 && average > 32 * run) {
+    const int64_t average = n_seq > 0 ? (rows + n_seq - 1) / n_seq : 0;
+    // Too few workgroups for long sequences: fewer channels each (64, whole lines of bfloat16) if that gives
+    // every CU one, as splitting them reads everything twice (16 sequences of 2048 steps of 1024 bfloat16
+    // channels: 50 us, 91 split; below 256 workgroups splitting wins, 2 of 32768 steps: 164 us, 1.6 ms whole).
+    auto run = [&] { return (int64_t)(64 / p.cl) * 8; };  // steps of one wave's tile
+    const int narrow = p.lg > 16 ? p.lg : 16;
+    if (p.parts == 1 && p.cl > narrow && n_seq * p.blocks < 256 && average > 16 * run()) {
+        const int per = p.cl / narrow;
+        if (n_seq * p.blocks * per >= 256) {
+            p.cl = narrow;
+            p.blocks = p.grouped ? (gates + p.cl / p.lg - 1) / (p.cl / p.lg)
+                                 : (int)(((int64_t)d + p.cl * V - 1) / (p.cl * V));
+        }
+    }
+    const int64_t units = n_seq * p.blocks;
+    // Waves of a workgroup, which share a tile: no more than a sequence has tiles, and fewer the more
+    // workgroups there are (65536 rays of 64 steps: 109 us with single waves, 139 with four).
+    p.waves = units >= 16384 || average <= run() ? 1 : units >= 1024 || average <= 4 * run() ? 4 : 8;
+    // Outputs past the caches where a step's are whole 64-byte sectors: the inputs stay in them (the gradient
+    // of 16 sequences of 2048 steps of 1024 channels 67 us, 83 else; but 16-byte rows 5 us against 33).
+    p.stream = p.cl * V * elt >= 64;
+    // A sequence to a lane's channels, walked alone, saves the exchanges between lanes that a tile needs: for
+    // the shortest always (35393 sequences of 2 steps of 32 channels: 10 us, 45 in tiles), else if there are
+    // lanes enough (16183 of 14: 9.7 us against 25; 256 rays of 64 by 16 channels: 18 against 7) and rows so
+    // short that a line serves the steps behind it (65536 rays of 64 steps of 4 channels: 80 us against 84;
+    // of 16 channels 169 against 122).
+    p.alone = average <= 4 || (units * p.cl >= 32768 && average <= (p.cl * V * elt <= 32 ? 128 : 16));
+    // In chunks: every input twice, against fewer workgroups than CUs.
+    if (units < kScanMaxSplit && average > 16 * run()) {
         p.waves = 4;
-        const int64_t each = (2048 + units - 1) / units, tile = 4 * run;  // chunks of a sequence
+        const int64_t each = (2048 + units - 1) / units, tile = 4 * run();  // chunks of a sequence
         p.chunk = ((average + each - 1) / each + tile - 1) / tile * tile;
         p.slots = rows / p.chunk + n_seq;
     }
