@@ -87,9 +87,14 @@ static void check_plan(const nerf::ScanArgs& a, bool backward) {
     CHECK((64 / p.cl * 8 * ld + a.d) * 4 < (int64_t)1 << 32);
     CHECK(!p.chunk || (!p.alone && a.n_seq < nerf::kScanMaxSplit));
     if (p.chunk) {
-        CHECK(p.slots >= a.rows / p.chunk + a.n_seq && p.chunk % (p.waves * (64 / p.cl) * 4) == 0);
-        std::memset(a.sum_a, 0, (size_t)p.slots * a.d * 4);
-        std::memset(a.sum_b, 0, (size_t)p.slots * a.d * 4);
+        CHECK(p.slots >= a.rows / p.chunk + a.n_seq && p.chunk == p.waves * (64 / p.cl) * (backward ? 4 : 8));
+        const size_t words = (size_t)p.slots * p.blocks * p.cl * V;
+        CHECK(reinterpret_cast<uintptr_t>(a.ticket) % 16 == 0 && reinterpret_cast<uintptr_t>(a.sum_a) % 16 == 0);
+        CHECK(reinterpret_cast<uintptr_t>(a.sum_b) % 16 == 0 && reinterpret_cast<uintptr_t>(a.state) % 16 == 0);
+        std::memset(a.ticket, 0, nerf::scan_chain_words(p) * 4);
+        std::memset(a.sum_a, 0, words * 4);
+        std::memset(a.sum_b, 0, words * 4);
+        std::memset(a.state, 0, words * 4);
     }
     if (backward && p.parts > 1 && a.rows > 0) std::memset(a.part_da, 0, (size_t)p.parts * a.rows * a.gates * 4);
     launched();

@@ -135,6 +135,9 @@ LARGE = [
     (_ragged(20, 330, 7), 1026, 9, True, True, "bf16", "f32", 0),
     (_ragged(70, 1400, 8), 64, 64, True, True, "bf16", "bf16", 0),      # chunks of more sequences than lanes
     (_ragged(70, 330, 9), 256, 1, False, True, "f32", "f32", 0),
+    ([9100], 256, 1, True, True, "bf16", "f32", 0),                    # more chunks than are looked at together
+    ([3000] * 4, 64, 64, False, True, "f32", "f32", 0),                # chunks of several sequences side by side
+    ([0, 9000, 0, 0, 1], 24, 24, False, True, "bf16", "bf16", 3),
 ]
 
 
@@ -390,6 +393,31 @@ def test_rows_far_apart(d, gates):
         assert (np.abs(_f64(dx) - rdx) <= 8 * rows * U * 2 * m).all()
         top = np.abs(_f64(th)).max() + np.abs(X).max()
         assert (np.abs(_f64(da) - rda) <= 8 * (rows + d) * U * m.sum() * top).all()
+
+
+def test_two_split_calls_at_once():
+    """Calls on two streams whose chunks wait for each other's neighbours only, results bit-equal to one at a time."""
+    torch = torch_cuda()
+    import volume_rendering_amd as v
+    say("two split scans at once")
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    mk = lambda *s: torch.randn(s, generator=gen, device="cuda")
+    jobs = []
+    for rows, d in ((20000, 512), (30000, 128)):
+        a, x = torch.sigmoid(mk(rows, d) + 3), mk(rows, d)
+        want, dx, da = torch.empty_like(x), torch.empty_like(x), torch.empty_like(a)
+        v.nerf_scan(a, x, want, mix=True)
+        v.nerf_scan_grad(x, a, x, want, da, dx, mix=True)
+        jobs.append((a, x, want, da, dx, [torch.empty_like(x) for _ in range(3)], torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for a, x, want, da, dx, (h, da2, dx2), stream in jobs:
+            with torch.cuda.stream(stream):
+                v.nerf_scan(a, x, h, mix=True)
+                v.nerf_scan_grad(x, a, x, h, da2, dx2, mix=True)
+    torch.cuda.synchronize()
+    for a, x, want, da, dx, (h, da2, dx2), _ in jobs:
+        assert torch.equal(h, want) and torch.equal(da2, da) and torch.equal(dx2, dx)
 
 
 def test_more_than_2_to_31_elements():

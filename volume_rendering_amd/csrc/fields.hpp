@@ -72,7 +72,7 @@ struct ScanPlan {
     int waves;       // waves that share a sequence (or chunk)
     bool alone;      // a lane walks a sequence alone
     bool stream;     // outputs are stored past the caches
-    int64_t chunk;   // steps of a chunk, 0: sequences are not split
+    int64_t chunk;   // steps of a chunk (one tile), 0: sequences are not split
     int64_t slots;   // chunks at most
 };
 struct ScanArgs {
@@ -94,23 +94,29 @@ struct ScanArgs {
     void* da;                  // [rows, gates]
     void* dx;                  // [rows, d]
     float* dh0;                // [n_seq, d] or NULL
-    float* sum_a;              // split: [slots, d] products of a chunk's gates, then its state before
-    float* sum_b;              // split: [slots, d] states of a chunk that began with 0
+    uint32_t* ticket;          // split: the next chunk to take (64 bits)
+    uint32_t* sum_a;           // split: per chunk, block and channel lane: the gates' products,
+    uint32_t* sum_b;           //   the states of a chunk that began with 0,
+    uint32_t* state;           //   and the states after the chunk
     float* part_da;            // [parts, rows, gates]
     ScanPlan p;
 };
-// The strides decide the lanes alone, not the workspace.
-ScanPlan scan_plan(int elt, int64_t rows, int64_t n_seq, int d, int gates);
+// The strides may take a plan's workspace away, but not change its size.
+ScanPlan scan_plan(int elt, int64_t rows, int64_t n_seq, int d, int gates, bool backward);
 void scan_plan_strides(ScanPlan& p, int64_t ld);
+// Steps of a lane, and waves of a chunk's workgroup.
+constexpr int scan_steps(bool backward) { return backward ? 4 : 8; }
+constexpr int kScanChainWaves = 8;
+// 32-bit words of a split call's workspace: the counter's four, and the chunks'.
+size_t scan_chain_words(const ScanPlan& p);
 constexpr int kScanMaxSplit = 256;  // sequences of a call that is split
 constexpr int64_t kScanMaxLd = (int64_t)1 << 26;  // elements
-size_t scan_workspace(const ScanPlan& p, int64_t rows, int d, int gates, bool backward);
+size_t scan_workspace(const ScanPlan& p, int64_t rows, int gates, bool backward);
 // gate_bf16 implies bf16.
 void launch_scan(bool bf16, bool gate_bf16, const ScanArgs& a, hipStream_t s);
 void launch_scan_grad(bool bf16, bool gate_bf16, const ScanArgs& a, hipStream_t s);
-// After the chunks' sums: each chunk's state before it (into sum_a) and the
-// sequences' final states (last, or NULL) from the initial ones (first, or NULL).
-void launch_scan_carry(const ScanArgs& a, const float* first, float* last, hipStream_t s);
+// The words of a split call's workspace before its chunks.
+void launch_scan_reset(const ScanArgs& a, hipStream_t s);
 
 // ---- gradient norm (clip.hip) ----
 size_t grad_norm_partials(const nerf_tensor* list, int n);

@@ -58,7 +58,8 @@ nerf_status check_scan(const char* who, const nerf_scan_cfg* c, bool offsets, bo
 // Rows of the hidden values start at whole 16 bytes of either form.
 size_t hidden_bytes(size_t pairs, int hidden) { return pairs * (((size_t)hidden + 7) & ~(size_t)7) * 6; }
 
-ScanArgs scan_args(const nerf_scan_cfg* c, const void* a, const void* x, const float* h0, const int32_t* offsets) {
+ScanArgs scan_args(const nerf_scan_cfg* c, const void* a, const void* x, const float* h0, const int32_t* offsets,
+                   bool backward) {
     ScanArgs s{};
     s.rows = c->rows;
     s.n_seq = c->n_seq;
@@ -75,19 +76,22 @@ ScanArgs scan_args(const nerf_scan_cfg* c, const void* a, const void* x, const f
     s.h0 = h0;
     s.ld_h = c->ld_h ? c->ld_h : c->d;
     s.ld_dh = c->ld_dh ? c->ld_dh : c->d;
-    s.p = scan_plan(elt_bytes(c->dtype), c->rows, c->n_seq, c->d, c->gates);
+    s.p = scan_plan(elt_bytes(c->dtype), c->rows, c->n_seq, c->d, c->gates, backward);
     scan_plan_strides(s.p, std::max(std::max(s.ld_a, s.ld_x), std::max(s.ld_h, s.ld_dh)));
     return s;
 }
 
 void scan_parts(ScanArgs& s, void* ws) {
-    float* f = static_cast<float*>(ws);
+    uint32_t* w = static_cast<uint32_t*>(ws);
     if (s.p.chunk) {
-        s.sum_a = f;
-        s.sum_b = f + s.p.slots * s.d;
-        f = s.sum_b + s.p.slots * s.d;
+        const size_t each = (scan_chain_words(s.p) - 4) / 3;
+        s.ticket = w;
+        s.sum_a = w + 4;
+        s.sum_b = s.sum_a + each;
+        s.state = s.sum_b + each;
+        w = s.state + each;
     }
-    s.part_da = f;
+    s.part_da = reinterpret_cast<float*>(w);
 }
 
 nerf_status check_list(const char* who, const nerf_tensor* list, int n) {
@@ -270,8 +274,9 @@ size_t nerf_scan_workspace_size(int64_t rows, int64_t n_seq, int d, int gates, i
         gates > d || d % gates)
         return 0;
     // (of either type of rows)
-    return std::max(scan_workspace(scan_plan(2, rows, n_seq, d, gates), rows, d, gates, backward != 0),
-                    scan_workspace(scan_plan(4, rows, n_seq, d, gates), rows, d, gates, backward != 0));
+    const bool b = backward != 0;
+    return std::max(scan_workspace(scan_plan(2, rows, n_seq, d, gates, b), rows, gates, b),
+                    scan_workspace(scan_plan(4, rows, n_seq, d, gates, b), rows, gates, b));
 }
 
 nerf_status nerf_scan(const nerf_scan_cfg* cfg, const void* a, const void* x, const int32_t* offsets, const float* h0,
@@ -285,11 +290,11 @@ nerf_status nerf_scan(const nerf_scan_cfg* cfg, const void* a, const void* x, co
     NERF_REQUIRE(aligned(a, elt_bytes(cfg->gate_dtype)) && aligned(x, b) && aligned(h, b) && aligned(offsets, 4) &&
                      aligned(h0, 4) && aligned(h_last, 4),
                  "%s: misaligned pointer", who);
-    ScanArgs s = scan_args(cfg, a, x, h0, offsets);
+    ScanArgs s = scan_args(cfg, a, x, h0, offsets, false);
     s.h = h;
     s.h_last = h_last;
     Workspace ws;
-    st = ws.take(who, workspace, workspace_bytes, scan_workspace(s.p, s.rows, s.d, s.gates, false), stream);
+    st = ws.take(who, workspace, workspace_bytes, scan_workspace(s.p, s.rows, s.gates, false), stream);
     if (st != NERF_OK) return st;
     scan_parts(s, ws.p);
     (void)hipGetLastError();
@@ -312,7 +317,7 @@ nerf_status nerf_scan_grad(const nerf_scan_cfg* cfg, const void* dh, const float
     NERF_REQUIRE(aligned(dh, b) && aligned(a, ba) && aligned(x, b) && aligned(h, b) && aligned(da, ba) &&
                      aligned(dx, b) && aligned(offsets, 4) && aligned(h0, 4) && aligned(dh_last, 4) && aligned(dh0, 4),
                  "%s: misaligned pointer", who);
-    ScanArgs s = scan_args(cfg, a, x, h0, offsets);
+    ScanArgs s = scan_args(cfg, a, x, h0, offsets, true);
     s.h = const_cast<void*>(h);
     s.dh = dh;
     s.dh_last = dh_last;
@@ -320,7 +325,7 @@ nerf_status nerf_scan_grad(const nerf_scan_cfg* cfg, const void* dh, const float
     s.dx = dx;
     s.dh0 = dh0;
     Workspace ws;
-    st = ws.take(who, workspace, workspace_bytes, scan_workspace(s.p, s.rows, s.d, s.gates, true), stream);
+    st = ws.take(who, workspace, workspace_bytes, scan_workspace(s.p, s.rows, s.gates, true), stream);
     if (st != NERF_OK) return st;
     scan_parts(s, ws.p);
     (void)hipGetLastError();

@@ -14,7 +14,7 @@ int pow2_at_least(int64_t v) {
 
 }  // namespace
 
-ScanPlan scan_plan(int elt, int64_t rows, int64_t n_seq, int d, int gates) {
+ScanPlan scan_plan(int elt, int64_t rows, int64_t n_seq, int d, int gates, bool backward) {
     ScanPlan p{};
     const int m = d / gates, wide = 4;
     p.grouped = gates < d;
@@ -40,19 +40,17 @@ ScanPlan scan_plan(int elt, int64_t rows, int64_t n_seq, int d, int gates) {
         }
     }
     const int64_t average = n_seq > 0 ? (rows + n_seq - 1) / n_seq : 0;
-    // Too few workgroups for long sequences: fewer channels each (64, whole lines of bfloat16) if that gives
-    // every CU one, as splitting them reads everything twice (16 sequences of 2048 steps of 1024 bfloat16
-    // channels: 50 us, 91 split; below 256 workgroups splitting wins, 2 of 32768 steps: 164 us, 1.6 ms whole).
     auto run = [&] { return (int64_t)(64 / p.cl) * 8; };  // steps of one wave's tile
+    auto lanes_of_channels = [&](int cl) {
+        p.cl = cl;
+        p.blocks = p.grouped ? (gates + cl / p.lg - 1) / (cl / p.lg) : (int)(((int64_t)d + cl * V - 1) / (cl * V));
+    };
+    // Too few workgroups for long sequences: fewer channels each (64, whole lines of bfloat16) if that gives
+    // every CU one (16 sequences of 2048 steps of 1024 bfloat16 channels: 50 us, 91 else).
     const int narrow = p.lg > 16 ? p.lg : 16;
-    if (p.parts == 1 && p.cl > narrow && n_seq * p.blocks < 256 && average > 16 * run()) {
-        const int per = p.cl / narrow;
-        if (n_seq * p.blocks * per >= 256) {
-            p.cl = narrow;
-            p.blocks = p.grouped ? (gates + p.cl / p.lg - 1) / (p.cl / p.lg)
-                                 : (int)(((int64_t)d + p.cl * V - 1) / (p.cl * V));
-        }
-    }
+    if (p.parts == 1 && p.cl > narrow && n_seq * p.blocks < 256 && average > 16 * run() &&
+        n_seq * p.blocks * (p.cl / narrow) >= 256)
+        lanes_of_channels(narrow);
     const int64_t units = n_seq * p.blocks;
     // Waves of a workgroup, which share a tile: no more than a sequence has tiles, and fewer the more
     // workgroups there are (65536 rays of 64 steps: 109 us with single waves, 139 with four).
@@ -66,26 +64,43 @@ ScanPlan scan_plan(int elt, int64_t rows, int64_t n_seq, int d, int gates) {
     // short that a line serves the steps behind it (65536 rays of 64 steps of 4 channels: 80 us against 84;
     // of 16 channels 169 against 122).
     p.alone = average <= 4 || (units * p.cl >= 32768 && average <= (p.cl * V * elt <= 32 ? 128 : 16));
-    // In chunks: every input twice, against fewer workgroups than CUs.
-    if (units < kScanMaxSplit && average > 16 * run()) {
-        p.waves = 4;
-        const int64_t each = (2048 + units - 1) / units, tile = 4 * run();  // chunks of a sequence
-        p.chunk = ((average + each - 1) / each + tile - 1) / tile * tile;
+    // In chunks of one tile, worked on at once: few sequences for the CUs (2 of 32768 steps of 1024 channels
+    // 125 us, by whole sequences 1.6 ms; the gradient of 46 of 392 steps of 33 15 us against 26).
+    if (units < kScanMaxSplit && average > 4 * run()) {
+        // A chunk waits for the one in front, so fewer channels and longer chunks shorten the chain; whole lines
+        // where there are chains enough (3 sequences of 300000 steps of 64 channels: 100 us with 16 channels a
+        // workgroup, 183 with 64; 2 of 32768 of 1024 channels: 125 us with 64, 141 with 32).
+        if (p.parts == 1) {
+            const int least = p.lg > 4 ? p.lg : 4;
+            if (p.cl > narrow) lanes_of_channels(narrow);
+            while (p.cl > least && n_seq * p.blocks < 8) lanes_of_channels(p.cl / 2);
+        }
+        p.waves = kScanChainWaves;
+        p.chunk = (int64_t)p.waves * (64 / p.cl) * scan_steps(backward);
         p.slots = rows / p.chunk + n_seq;
     }
     return p;
 }
 
 // The steps of a wave's tile are within 32-bit byte offsets of each other: rows
-// far apart get all lanes for their channels, and so eight steps a tile.
+// far apart get all lanes for their channels, and so eight steps a tile, and
+// whole sequences, as chunks would be more than the workspace has room for.
 void scan_plan_strides(ScanPlan& p, int64_t ld) {
-    if ((64 / p.cl) * 8 * ld + 65536 > (int64_t)1 << 30) p.cl = 64;
+    if ((64 / p.cl) * 8 * ld + 65536 > (int64_t)1 << 30) {
+        p.cl = 64;
+        p.chunk = 0;
+    }
 }
 
-size_t scan_workspace(const ScanPlan& p, int64_t rows, int d, int gates, bool backward) {
-    size_t floats = p.chunk ? 2 * (size_t)p.slots * (size_t)d : 0;
-    if (backward && p.parts > 1) floats += (size_t)p.parts * (size_t)rows * (size_t)gates;
-    return floats * sizeof(float);
+size_t scan_chain_words(const ScanPlan& p) {
+    const size_t each = (size_t)p.slots * p.blocks * p.cl * (p.vec ? 4 : 1);
+    return 4 + 3 * ((each + 3) & ~(size_t)3);
+}
+
+size_t scan_workspace(const ScanPlan& p, int64_t rows, int gates, bool backward) {
+    size_t words = p.chunk ? scan_chain_words(p) : 0;
+    if (backward && p.parts > 1) words += (size_t)p.parts * (size_t)rows * (size_t)gates;
+    return words * sizeof(float);
 }
 
 }  // namespace nerf
