@@ -736,7 +736,9 @@ size_t nerf_scan_workspace_size(int64_t rows, int64_t n_seq, int d, int gates, i
 /* a: device [rows, gates]; x: device [rows, d]; offsets: device int32
  * [n_seq + 1] or NULL; h0: device float32 [n_seq, d] or NULL (0); h: device
  * [rows, d]; h_last: device float32 [n_seq, d] or NULL, the state after each
- * sequence; it may be h0 (a stream's state, updated in place).  Errors: null
+ * sequence; it may be h0 (a stream's state, updated in place).  Few long
+ * sequences are cut into chunks whose workgroups wait for one another through
+ * the workspace, which is why two calls at once must not share one.  Errors: null
  * pointers, bad dtypes, sizes, strides or alignment, rows that are not n_seq
  * equal sequences, h == x or a, workspace too small; NERF_ERR_UNSUPPORTED for
  * bfloat16 gates of float32 rows and row strides above 2^26 elements. */

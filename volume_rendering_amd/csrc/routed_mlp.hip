@@ -15,6 +15,9 @@
 // pairs at a time, and a third kernel adds up the samples' terms.
 // Hidden values keep 24 bits between the kernels (rounding them to bfloat16 would
 // add an error as large as the output's own rounding, and saves only L2 traffic).
+// Measured: one sample through 2 of 16 experts 1024 -> 4096 -> 1024, bfloat16,
+// 11.6 us (33.6 MB, 2.9 TB/s); 16 samples through 4 of 64 gated experts of 1024, 60 us
+// (256 MB, 4.3 TB/s); 64 through 2 of 8 experts 1024 -> 4096 -> 1024, 69 us (134 MB).
 #include <hip/hip_runtime.h>
 
 #include <cfloat>

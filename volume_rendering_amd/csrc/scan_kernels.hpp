@@ -237,7 +237,7 @@ __device__ __forceinline__ Affine<NA, V> after(const Affine<NA, V>& first, const
 // take words away; the wait then ends with NaN.
 // ---------------------------------------------------------------------------
 constexpr uint32_t kNotYet = 0xFFFFFFFFu;
-constexpr int64_t kWaitTicks = 200000000;  // 2 s of the 100 MHz clock
+constexpr int kLooks = 1 << 21;  // at least a second of a running wave, however long it was set aside
 
 __device__ __forceinline__ void leave(uint32_t* p, float f) {
     const uint32_t w = __float_as_uint(f);
@@ -247,8 +247,8 @@ __device__ __forceinline__ uint32_t look(const uint32_t* p) {
     return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 // Looks again until the words of all lanes are there.
-__device__ __forceinline__ float wait_for(const uint32_t* p, uint32_t w, int64_t start) {
-    while (!__all(w != kNotYet) && wall_clock64() - start < kWaitTicks) {
+__device__ __forceinline__ float wait_for(const uint32_t* p, uint32_t w, int& looks) {
+    while (!__all(w != kNotYet) && --looks > 0) {
         __builtin_amdgcn_s_sleep(1);
         w = look(p);
     }
@@ -257,12 +257,12 @@ __device__ __forceinline__ float wait_for(const uint32_t* p, uint32_t w, int64_t
 
 // How many chunks in front the nearest state is (of the channel whose word is
 // `first`): 1 to `most`.  By a wave.
-__device__ __forceinline__ int nearest_state(const uint32_t* first, int64_t back, int most, int lane, int64_t start) {
+__device__ __forceinline__ int nearest_state(const uint32_t* first, int64_t back, int most, int lane, int& looks) {
     for (;;) {
         const bool in = lane < most;
         const uint64_t have = __ballot(in && look(first - (in ? lane + 1 : 1) * back) != kNotYet);
         if (have) return __builtin_ctzll(have) + 1;
-        if (wall_clock64() - start >= kWaitTicks) return 1;
+        if (--looks <= 0) return 1;
         __builtin_amdgcn_s_sleep(1);
     }
 }
@@ -535,11 +535,11 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W, CHAIN && sizeof(T) == 2
                     leave(a.sum_b + words + word, B);
                 }
                 if (q.c0 > 0) {
-                    const int64_t start = wall_clock64();
+                    int looks = kLooks;
                     if (wave == 0) {
                         const uint32_t front = (uint32_t)q.c0 / (uint32_t)a.p.chunk, window = kScanLooked / width;
                         const int most = front < 64 && front < window ? (int)front : window < 64 ? (int)window : 64;
-                        nearest = nearest_state(a.state + words, back, most, lane, start);
+                        nearest = nearest_state(a.state + words, back, most, lane, looks);
                     }
                     __syncthreads();
                     const int k = __builtin_amdgcn_readfirstlane(nearest);
@@ -550,11 +550,11 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W, CHAIN && sizeof(T) == 2
                         const int64_t at = words - (k - 1 - p / groups) * back + (p % groups) * 64;
                         const uint32_t wa = look(a.sum_a + at + in), wb = look(a.sum_b + at + in);
                         const int to = p / groups * width + p % groups * 64 + in;
-                        between_a[to] = wait_for(a.sum_a + at + in, wa, start);
-                        between_b[to] = wait_for(a.sum_b + at + in, wb, start);
+                        between_a[to] = wait_for(a.sum_a + at + in, wa, looks);
+                        between_b[to] = wait_for(a.sum_b + at + in, wb, looks);
                     }
                     if (k > 1) __syncthreads();
-                    if (joins) s1 = wait_for(a.state + (words - k * back) + word, w, start);
+                    if (joins) s1 = wait_for(a.state + (words - k * back) + word, w, looks);
                     if (joins)
 #pragma unroll 4
                         for (int p = 0; p < k - 1; ++p) s1 = fmaf(between_a[p * width + word], s1, between_b[p * width + word]);

@@ -56,7 +56,8 @@ ScanPlan scan_plan(int elt, int64_t rows, int64_t n_seq, int d, int gates, bool 
     // workgroups there are (65536 rays of 64 steps: 109 us with single waves, 139 with four).
     p.waves = units >= 16384 || average <= run() ? 1 : units >= 1024 || average <= 4 * run() ? 4 : 8;
     // Outputs past the caches where a step's are whole 64-byte sectors: the inputs stay in them (the gradient
-    // of 16 sequences of 2048 steps of 1024 channels 67 us, 83 else; but 16-byte rows 5 us against 33).
+    // of 16 sequences of 2048 steps of 1024 channels 67 us, 83 else; but 16-byte rows 5 us against 33).  Before
+    // chunks of fewer channels, whose neighbours write the rest (3 of 300000 steps of 64: 101 us, 128 else).
     p.stream = p.cl * V * elt >= 64;
     // A sequence to a lane's channels, walked alone, saves the exchanges between lanes that a tile needs: for
     // the shortest always (35393 sequences of 2 steps of 32 channels: 10 us, 45 in tiles), else if there are
