@@ -395,6 +395,42 @@ def test_rows_far_apart(d, gates):
         assert (np.abs(_f64(da) - rda) <= 8 * (rows + d) * U * m.sum() * top).all()
 
 
+@pytest.mark.parametrize("lens", [[5, 0, 40], [3000, 3, 5990], [4] * 300])
+def test_rows_in_front_of_the_first_sequence(lens):
+    """Rows before the first sequence and behind the last are left as they are."""
+    torch = torch_cuda()
+    import volume_rendering_amd as v
+    say(f"scan behind other rows {lens[:3]}")
+    g = np.random.default_rng(len(lens))
+    lead, d, n = 70, 20, len(lens)
+    off = lead + _offsets(g, lens)
+    rows = int(off[-1]) + 9
+    a, x, h0 = _inputs(g, rows, d, d, n)
+    ta, tx, th0 = _put(a, "f32"), _put(x, "f32"), _put(h0, "f32")
+    a, x, h0 = _f64(ta), _f64(tx), _f64(th0)
+    toff = torch.from_numpy(off.astype(np.int32)).cuda()
+    h, da, dx = (torch.full((rows, d), 7.0, device="cuda") for _ in range(3))
+    v.nerf_scan(ta, tx, h, h0=th0, offsets=toff)
+    ref, _ = O.scan(a, x, off, h0)
+    _, E, _ = _bounds(a, x, off, h0, False)
+    inside = slice(lead, int(off[-1]))
+    hh = _f64(h)
+    _close("h", hh[inside], ref[inside], (E + U * (np.abs(ref) + E))[inside])
+    v.nerf_scan_grad(tx, ta, None, h, da, dx, h0=th0, offsets=toff)
+    _, rdx, _ = O.scan_grad(x, None, a, x, np.nan_to_num(hh), h0, off)
+    _, E, _ = _bounds(a, a * x, off, np.zeros((n, d)), True)
+    before = np.zeros((rows, d))  # errors of what flows into each row
+    M, _, _ = _bounds(a, a * x, off, np.zeros((n, d)), True)
+    mags = np.zeros((rows, d))
+    for s in range(n):
+        before[off[s]:max(off[s], off[s + 1] - 1)] = E[off[s] + 1:off[s + 1]]
+        mags[off[s]:max(off[s], off[s + 1] - 1)] = M[off[s] + 1:off[s + 1]]
+    tol = before + 2 * U * (np.abs(x) + mags)
+    _close("dx", _f64(dx)[inside], rdx[inside], tol[inside])
+    for t in (h, da, dx):
+        assert (t[:lead] == 7.0).all() and (t[int(off[-1]):] == 7.0).all()
+
+
 def test_two_split_calls_at_once():
     """Calls on two streams whose chunks wait for each other's neighbours only, results bit-equal to one at a time."""
     torch = torch_cuda()

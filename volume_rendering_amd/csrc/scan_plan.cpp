@@ -66,8 +66,10 @@ ScanPlan scan_plan(int elt, int64_t rows, int64_t n_seq, int d, int gates, bool 
     // of 16 channels 169 against 122).
     p.alone = average <= 4 || (units * p.cl >= 32768 && average <= (p.cl * V * elt <= 32 ? 128 : 16));
     // In chunks of one tile, worked on at once: few sequences for the CUs (2 of 32768 steps of 1024 channels
-    // 125 us, by whole sequences 1.6 ms; the gradient of 46 of 392 steps of 33 15 us against 26).
-    if (units < kScanMaxSplit && average > 4 * run()) {
+    // 123 us, by whole sequences 1.6 ms; the gradient of 46 of 392 steps of 33 15 us against 26), if they are
+    // longer than two tiles of eight waves (30 of 200 steps of 256 channels 11.3 us against 15.7, of 100 10.2
+    // against 9.5: a chunk's words have to be made ready first).
+    if (units < kScanMaxSplit && average > 16 * (64 / p.cl) * scan_steps(backward)) {
         // A chunk waits for the one in front, so fewer channels and longer chunks shorten the chain; whole lines
         // where there are chains enough (3 sequences of 300000 steps of 64 channels: 100 us with 16 channels a
         // workgroup, 183 with 64; 2 of 32768 of 1024 channels: 125 us with 64, 141 with 32).
