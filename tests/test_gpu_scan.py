@@ -135,6 +135,7 @@ LARGE = [
     (_ragged(20, 330, 7), 1026, 9, True, True, "bf16", "f32", 0),
     (_ragged(70, 1400, 8), 64, 64, True, True, "bf16", "bf16", 0),      # chunks of more sequences than lanes
     (_ragged(70, 330, 9), 256, 1, False, True, "f32", "f32", 0),
+    (_ragged(130, 200, 10), 160, 1, False, True, "f32", "f32", 0),      # whole ones of a gate of 40 lanes
     ([9100], 256, 1, True, True, "bf16", "f32", 0),                    # more chunks than are looked at together
     ([3000] * 4, 64, 64, False, True, "f32", "f32", 0),                # chunks of several sequences side by side
     ([0, 9000, 0, 0, 1], 24, 24, False, True, "bf16", "bf16", 3),

@@ -69,7 +69,10 @@ ScanPlan scan_plan(int elt, int64_t rows, int64_t n_seq, int d, int gates, bool 
     // 123 us, by whole sequences 1.6 ms; the gradient of 46 of 392 steps of 33 15 us against 26), if they are
     // longer than two tiles of eight waves (30 of 200 steps of 256 channels 11.3 us against 15.7, of 100 10.2
     // against 9.5: a chunk's words have to be made ready first).
-    if (units < kScanMaxSplit && average > 16 * (64 / p.cl) * scan_steps(backward)) {
+    // Chunks of one wide gate's channels are short, and of given offsets come sequence after sequence: fewer
+    // sequences then (of 1551 steps of 160 channels 64 take 81 us against 113, 128 take 144 against 115).
+    const int64_t most = p.parts > 1 || narrow > 16 ? 96 : kScanMaxSplit;
+    if (units < most && average > 16 * (64 / p.cl) * scan_steps(backward)) {
         // A chunk waits for the one in front, so fewer channels and longer chunks shorten the chain; whole lines
         // where there are chains enough (3 sequences of 300000 steps of 64 channels: 100 us with 16 channels a
         // workgroup, 183 with 64; 2 of 32768 of 1024 channels: 125 us with 64, 141 with 32).
