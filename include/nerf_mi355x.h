@@ -701,7 +701,9 @@ size_t nerf_routed_mlp_workspace_size(int64_t n, int k, int hidden, int d_out);
  * ids: device int32 [n, k]; weights: device float32 [n, k] or NULL (all 1); w1:
  * device [n_experts, hidden, d_in] (gated: 2 hidden rows); w2: device
  * [n_experts, d_out, hidden]; b1, b2: device float32 [n_experts, rows] or NULL;
- * out: device [n, d_out].  Hidden values keep float32's 24 bits.  workspace: device,
+ * out: device [n, d_out].  Hidden values keep float32's 24 bits (in bfloat16 calls of
+ * more than two pairs per expert: from 2^-109 on; an infinite weight gives what
+ * the formula gives from 2^-96 on and for 0, else an infinity or NaN).  workspace: device,
  * 16-byte aligned, at least nerf_routed_mlp_workspace_size bytes, or NULL
  * (allocated stream-ordered).  Errors: null pointers, bad dtype, act, sizes,
  * strides or alignment, workspace too small; NERF_ERR_UNSUPPORTED for more than

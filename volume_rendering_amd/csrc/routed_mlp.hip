@@ -258,15 +258,26 @@ __device__ __forceinline__ void matrix_dots(f32x4 (&acc)[NG], const T* w, const 
 }
 
 // The leading eight bits of what is left, three times: bfloat16 numbers that add
-// up to a float32 one (an infinity or NaN: itself, then 0).
+// up to a float32 one.  A part of 0 beside others would make NaN of an infinite
+// weight's product, so where nothing is left the part before is shared out (from
+// 2^-96 on halves and quarters of eight bits are exact and normal; below, such a
+// product is infinite or NaN), and an infinity or NaN is all three parts.
 __device__ __forceinline__ void three_parts(float v, __bf16 (&part)[3]) {
-    const bool finite = fabsf(v) <= FLT_MAX;
-    const float top = __uint_as_float(__float_as_uint(v) & 0xFFFF0000u);
-    part[0] = (__bf16)(finite ? top : v);
-    v = finite ? v - top : 0.0f;
-    const float mid = __uint_as_float(__float_as_uint(v) & 0xFFFF0000u);
-    part[1] = (__bf16)mid;
-    part[2] = (__bf16)(v - mid);
+    const float top = __uint_as_float(__float_as_uint(v) & 0xFFFF0000u), rest = v - top;
+    const float mid = __uint_as_float(__float_as_uint(rest) & 0xFFFF0000u), low = rest - mid;
+    float p[3] = {top, mid, low};
+    if (!(fabsf(v) <= FLT_MAX)) {
+        p[0] = p[1] = p[2] = v;
+    } else if (fabsf(v) >= 0x1p-96f) {
+        if (rest == 0.0f) {
+            p[0] = 0.5f * top;
+            p[1] = p[2] = 0.25f * top;
+        } else if (low == 0.0f) {
+            p[1] = p[2] = 0.5f * mid;
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < 3; ++t) part[t] = (__bf16)p[t];
 }
 
 // Calls f with the number of 16-vector sets that `count` (at most kGroup) pairs take: 1, 2 or 4.
