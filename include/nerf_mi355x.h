@@ -721,8 +721,11 @@ nerf_status nerf_routed_mlp(const nerf_routed_layer* layer, const void* x, const
  * Sequence s is rows offsets[s] .. offsets[s+1]-1, or, with offsets NULL, the
  * s-th of n_seq equal ones; an empty one has state h0; rows outside every
  * sequence keep what they hold.  Offsets out of range are kept in range.
- * States are carried across runs of steps by products of their gates: those
- * must stay in float32's range, as they do for gates of magnitude up to 1. */
+ * States are carried across runs of steps by products of their gates, and a
+ * run's terms are summed from 0: the products, and the sums of the terms'
+ * magnitudes, must stay below float32's largest number (gates of magnitude up
+ * to 1 keep the products there).  Infinite inputs and states go on as in the
+ * formula; a product below 2^-149 counts as that unless a gate is 0. */
 typedef struct {
     int32_t dtype;        /* of x, h, dh and dx */
     int32_t gate_dtype;   /* of a and da: dtype, or NERF_F32 */

@@ -211,13 +211,20 @@ template <int NA, int V>
 struct Affine {
     float A[NA], B[V];
 };
+// Products of gates.  One of gates that are not 0 stays so when it leaves
+// float32's range, as an infinite state stays infinite behind it; a finite state
+// gets 2^-149 of itself at most, half of which such a product is off by anyway.
+__device__ __forceinline__ float not_zero(float p, bool zero) {
+    return p == 0.0f && !zero ? copysignf(0x1p-149f, p) : p;
+}
+__device__ __forceinline__ float times(float a, float b) { return not_zero(a * b, a == 0.0f || b == 0.0f); }
 template <int NA, int V>
 __device__ __forceinline__ Affine<NA, V> after(const Affine<NA, V>& first, const Affine<NA, V>& then) {
     Affine<NA, V> r;
 #pragma unroll
     for (int v = 0; v < V; ++v) r.B[v] = fmaf(then.A[NA == 1 ? 0 : v], first.B[v], then.B[v]);
 #pragma unroll
-    for (int v = 0; v < NA; ++v) r.A[v] = then.A[v] * first.A[v];
+    for (int v = 0; v < NA; ++v) r.A[v] = times(then.A[v], first.A[v]);
     return r;
 }
 
@@ -450,9 +457,10 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W, CHAIN && sizeof(T) == 2
                 const float in = Some<T, V>::get(f.in[j], v);
                 return !BACK && a.mix ? in * (1.0f - gate_of(j, v)) : in;
             };
-            Aff lanes;  // the lane's run as one step
+            Aff lanes;         // the lane's run as one step
+            float least[NA];  // the smallest gate's magnitude
 #pragma unroll
-            for (int v = 0; v < NA; ++v) lanes.A[v] = 1.0f;
+            for (int v = 0; v < NA; ++v) lanes.A[v] = least[v] = 1.0f;
 #pragma unroll
             for (int v = 0; v < V; ++v) lanes.B[v] = 0.0f;
             auto fold = [&](auto whole) {
@@ -465,8 +473,13 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W, CHAIN && sizeof(T) == 2
                             lanes.B[v] = BACK ? A * (lanes.B[v] + in) : fmaf(A, lanes.B[v], in);
                         }
 #pragma unroll
-                        for (int v = 0; v < NA; ++v) lanes.A[v] *= gate_of(j, v);
+                        for (int v = 0; v < NA; ++v) {
+                            lanes.A[v] *= gate_of(j, v);
+                            least[v] = fminf(least[v], fabsf(gate_of(j, v)));
+                        }
                     }
+#pragma unroll
+                for (int v = 0; v < NA; ++v) lanes.A[v] = not_zero(lanes.A[v], least[v] == 0.0f);
             };
             if constexpr (AHEAD) {
                 f = next;
@@ -525,12 +538,15 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W, CHAIN && sizeof(T) == 2
                 const int word = wave * 64 + lane < width ? wave * 64 + lane : 0, cw = word / V, v = word % V;
                 float A = 1.0f, B = 0.0f, s1 = 0.0f;
                 if (joins) {
+                    float least = 1.0f;
 #pragma unroll
                     for (int w = 0; w < W; ++w) {
                         const float m = total[0][w][cw].A[NA == 1 ? 0 : v];
                         B = fmaf(m, B, total[0][w][cw].B[v]);
                         A *= m;
+                        least = fminf(least, fabsf(m));
                     }
+                    A = not_zero(A, least == 0.0f);
                     leave(a.sum_a + words + word, A);
                     leave(a.sum_b + words + word, B);
                 }
