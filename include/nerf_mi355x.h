@@ -707,7 +707,9 @@ size_t nerf_routed_mlp_workspace_size(int64_t n, int k, int hidden, int d_out);
  * 16-byte aligned, at least nerf_routed_mlp_workspace_size bytes, or NULL
  * (allocated stream-ordered).  Errors: null pointers, bad dtype, act, sizes,
  * strides or alignment, workspace too small; NERF_ERR_UNSUPPORTED for more than
- * 512 pairs or 4096 experts. */
+ * 512 pairs (nerf_expert_linear takes more, but has no gated hidden layer and no
+ * gradient of one: with its two products the caller gates in between) or 4096
+ * experts. */
 nerf_status nerf_routed_mlp(const nerf_routed_layer* layer, const void* x, const int32_t* ids, const float* weights,
                             int64_t n, const void* w1, const float* b1, const void* w2, const float* b2, void* out,
                             void* workspace, size_t workspace_bytes, void* stream);

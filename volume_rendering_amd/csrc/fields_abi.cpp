@@ -229,8 +229,9 @@ nerf_status nerf_routed_mlp(const nerf_routed_layer* L, const void* x, const int
     if (L->n_experts > NERF_MAX_EXPERTS)
         return nerf_fail(NERF_ERR_UNSUPPORTED, "%s: n_experts %d above %d", who, L->n_experts, NERF_MAX_EXPERTS);
     if (n > NERF_FEW_PAIRS / L->k)
-        return nerf_fail(NERF_ERR_UNSUPPORTED, "%s: %lld x %d pairs (at most %d: nerf_expert_linear takes more)", who,
-                         (long long)n, L->k, NERF_FEW_PAIRS);
+        return nerf_fail(NERF_ERR_UNSUPPORTED, "%s: %lld x %d pairs (at most %d: nerf_expert_linear takes more%s)", who,
+                         (long long)n, L->k, NERF_FEW_PAIRS,
+                         L->act == NERF_ACT_GATED ? ", but has no gated hidden layer: its caller gates in between" : "");
     if (n == 0) return NERF_OK;
     const int b = elt_bytes(L->dtype);
     NERF_REQUIRE(x && ids && w1 && w2 && out, "%s: NULL input or output", who);
