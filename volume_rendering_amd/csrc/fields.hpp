@@ -103,7 +103,7 @@ struct ScanArgs {
 };
 // The strides may take a plan's workspace away, but not change its size.
 ScanPlan scan_plan(int elt, int64_t rows, int64_t n_seq, int d, int gates, bool backward);
-void scan_plan_strides(ScanPlan& p, int64_t ld);
+void scan_plan_strides(ScanPlan& p, int d, int gates, int64_t ld);
 // Steps of a lane, and waves of a chunk's workgroup.
 constexpr int scan_steps(bool backward) { return backward ? 4 : 8; }
 constexpr int kScanChainWaves = 8;

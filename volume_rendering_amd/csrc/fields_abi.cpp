@@ -77,7 +77,7 @@ ScanArgs scan_args(const nerf_scan_cfg* c, const void* a, const void* x, const f
     s.ld_h = c->ld_h ? c->ld_h : c->d;
     s.ld_dh = c->ld_dh ? c->ld_dh : c->d;
     s.p = scan_plan(elt_bytes(c->dtype), c->rows, c->n_seq, c->d, c->gates, backward);
-    scan_plan_strides(s.p, std::max(std::max(s.ld_a, s.ld_x), std::max(s.ld_h, s.ld_dh)));
+    scan_plan_strides(s.p, c->d, c->gates, std::max(std::max(s.ld_a, s.ld_x), std::max(s.ld_h, s.ld_dh)));
     return s;
 }
 

@@ -12,6 +12,14 @@ int pow2_at_least(int64_t v) {
     return p;
 }
 
+// A block of `cl` channel lanes, and as many as the channels take (no gate over
+// several blocks).
+void lanes_of_channels(ScanPlan& p, int d, int gates, int cl) {
+    const int V = p.vec ? 4 : 1;
+    p.cl = cl;
+    p.blocks = p.grouped ? (gates + cl / p.lg - 1) / (cl / p.lg) : (int)(((int64_t)d + cl * V - 1) / (cl * V));
+}
+
 }  // namespace
 
 ScanPlan scan_plan(int elt, int64_t rows, int64_t n_seq, int d, int gates, bool backward) {
@@ -41,16 +49,12 @@ ScanPlan scan_plan(int elt, int64_t rows, int64_t n_seq, int d, int gates, bool 
     }
     const int64_t average = n_seq > 0 ? (rows + n_seq - 1) / n_seq : 0;
     auto run = [&] { return (int64_t)(64 / p.cl) * 8; };  // steps of one wave's tile
-    auto lanes_of_channels = [&](int cl) {
-        p.cl = cl;
-        p.blocks = p.grouped ? (gates + cl / p.lg - 1) / (cl / p.lg) : (int)(((int64_t)d + cl * V - 1) / (cl * V));
-    };
     // Too few workgroups for long sequences: fewer channels each (64, whole lines of bfloat16) if that gives
     // every CU one (16 sequences of 2048 steps of 1024 bfloat16 channels: 50 us, 91 else).
     const int narrow = p.lg > 16 ? p.lg : 16;
     if (p.parts == 1 && p.cl > narrow && n_seq * p.blocks < 256 && average > 16 * run() &&
         n_seq * p.blocks * (p.cl / narrow) >= 256)
-        lanes_of_channels(narrow);
+        lanes_of_channels(p, d, gates, narrow);
     const int64_t units = n_seq * p.blocks;
     // Waves of a workgroup, which share a tile: no more than a sequence has tiles, and fewer the more
     // workgroups there are (65536 rays of 64 steps: 109 us with single waves, 139 with four).
@@ -78,8 +82,8 @@ ScanPlan scan_plan(int elt, int64_t rows, int64_t n_seq, int d, int gates, bool 
         // workgroup, 183 with 64; 2 of 32768 of 1024 channels: 125 us with 64, 141 with 32).
         if (p.parts == 1) {
             const int least = p.lg > 4 ? p.lg : 4;
-            if (p.cl > narrow) lanes_of_channels(narrow);
-            while (p.cl > least && n_seq * p.blocks < 8) lanes_of_channels(p.cl / 2);
+            if (p.cl > narrow) lanes_of_channels(p, d, gates, narrow);
+            while (p.cl > least && n_seq * p.blocks < 8) lanes_of_channels(p, d, gates, p.cl / 2);
         }
         p.waves = kScanChainWaves;
         p.chunk = (int64_t)p.waves * (64 / p.cl) * scan_steps(backward);
@@ -91,9 +95,9 @@ ScanPlan scan_plan(int elt, int64_t rows, int64_t n_seq, int d, int gates, bool 
 // The steps of a wave's tile are within 32-bit byte offsets of each other: rows
 // far apart get all lanes for their channels, and so eight steps a tile, and
 // whole sequences, as chunks would be more than the workspace has room for.
-void scan_plan_strides(ScanPlan& p, int64_t ld) {
+void scan_plan_strides(ScanPlan& p, int d, int gates, int64_t ld) {
     if ((64 / p.cl) * 8 * ld + 65536 > (int64_t)1 << 30) {
-        p.cl = 64;
+        lanes_of_channels(p, d, gates, 64);  // (a gate over several blocks has them already)
         p.chunk = 0;
     }
 }
