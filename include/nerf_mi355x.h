@@ -709,7 +709,10 @@ size_t nerf_routed_mlp_workspace_size(int64_t n, int k, int hidden, int d_out);
  * strides or alignment, workspace too small; NERF_ERR_UNSUPPORTED for more than
  * 512 pairs (nerf_expert_linear takes more, but has no gated hidden layer and no
  * gradient of one: with its two products the caller gates in between) or 4096
- * experts. */
+ * experts.  For samples that are spread over the experts, a few each: where most
+ * pairs are of one among many experts, and for wide bfloat16 layers from 64 to 256
+ * pairs on, nerf_route_plan, nerf_expert_linear and nerf_route_combine are faster
+ * (512 pairs of one of 256 experts 62 us against 775). */
 nerf_status nerf_routed_mlp(const nerf_routed_layer* layer, const void* x, const int32_t* ids, const float* weights,
                             int64_t n, const void* w1, const float* b1, const void* w2, const float* b2, void* out,
                             void* workspace, size_t workspace_bytes, void* stream);
@@ -723,6 +726,10 @@ nerf_status nerf_routed_mlp(const nerf_routed_layer* layer, const void* x, const
  * Sequence s is rows offsets[s] .. offsets[s+1]-1, or, with offsets NULL, the
  * s-th of n_seq equal ones; an empty one has state h0; rows outside every
  * sequence keep what they hold.  Offsets out of range are kept in range.
+ * Lengths may be any, but the work is shared out by their average, rows / n_seq:
+ * a sequence many times longer than that is walked by few lanes (one of 30,000
+ * steps among 10,000 of up to one 4.9 ms, 17 us by itself), so give such ones a call
+ * of their own.
  * States are carried across runs of steps by products of their gates, and a
  * run's terms are summed from 0: the products, and the sums of the terms'
  * magnitudes, must stay below float32's largest number (gates of magnitude up
@@ -785,8 +792,9 @@ nerf_status nerf_grad_norm(const nerf_tensor* list, int n, float* norm, void* wo
                            void* stream);
 
 /* norm as above, and dst = src * min(1, max_norm / norm) for every tensor.  A
- * NaN norm makes every element NaN; with an infinite one finite elements become
- * 0.  Tensors scaled in place by 1 are not touched.  Errors: as nerf_grad_norm,
+ * NaN norm makes every element NaN; with an infinite element finite ones become 0.
+ * The factor is that of the float64 norm, also where norm itself is beyond
+ * float32 and infinite.  Tensors scaled in place by 1 are not touched.  Errors: as nerf_grad_norm,
  * a NULL destination, max_norm negative or NaN, a destination that overlaps
  * another tensor's source or destination, or its own source in part. */
 nerf_status nerf_grad_clip(const nerf_tensor* list, int n, float max_norm, float* norm, void* workspace,

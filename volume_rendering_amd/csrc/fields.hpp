@@ -64,7 +64,7 @@ void launch_routed_mlp(bool bf16, const MlpArgs& a, hipStream_t s);
 // How a call is cut up.  Lanes of a wave are CL channel lanes (V channels each)
 // times 64 / CL runs of consecutive steps; a gate's channels take LG of them.
 struct ScanPlan {
-    bool vec;        // V elements of 8 bytes together, or 1
+    bool vec;        // V is 4 (8 bytes of bfloat16, 16 of float32), or 1
     bool grouped;    // fewer gates than channels
     int cl, lg;      // channel lanes, lanes of a gate's channels (powers of two)
     int blocks;      // channel blocks: workgroups side by side

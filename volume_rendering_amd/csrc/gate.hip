@@ -7,10 +7,11 @@
 // An expert whose logit is -inf is never chosen; a choice without an expert
 // has id -1 and weight 0.
 // A row is read once and stays in registers: k rounds of a maximum over its lanes,
-// which bound the kernel where rows are short (262144 rows of 16 bfloat16 logits, 2
-// chosen, 12.6 MB: 5.4 us, 2.3 TB/s; 16384 of 256, 8 chosen: 10.2 us), and a launch's
-// latency for few rows (one: 4 us).  The gradient reads a row at most once: 20011
-// of 61 float32 logits in 3.7 us, 2.8 TB/s.
+// which bound the kernel (in a graph of calls, 262144 rows of 16 bfloat16 logits, 2
+// chosen, 12.6 MB: 6.2 us, 2.0 TB/s; 16384 of 256, 8 chosen: 10.9 us; 4096 of 4096:
+// 28 us, four times the read, as every round looks at all of a lane's keys), and a
+// launch's latency for few rows (one: 2.6 us).  The gradient reads a row at most once:
+// 20011 of 61 float32 logits, 10.5 MB, in 4.8 us, 2.2 TB/s.
 #include <hip/hip_runtime.h>
 
 #include <cmath>

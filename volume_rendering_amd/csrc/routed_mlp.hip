@@ -1,23 +1,29 @@
 // The whole two-layer routed field for a few samples, for gfx950:
 //   out_t = sum_j w_tj (W2_e act(W1_e x_t + b1_e) + b2_e),   e = ids_tj.
 // Every weight of an expert that some pair (sample, choice) uses is read from
-// memory once; that read bounds the kernels, and for one sample the launches and
-// one chain of dependent loads each.  Up to 64 pairs are sorted by expert by every
+// memory once; with few pairs per expert that read bounds the kernels, and for one
+// sample the launches and one chain of dependent loads each.  Up to 64 pairs are sorted by expert by every
 // workgroup itself, in LDS, which is cheaper than a kernel in front; more (the work
 // grows with their square) by a kernel of their own.
-// With up to two pairs per expert (on average) two kernels of dot products, whose
-// weights a wave reads in whole lines.  First the hidden layer: workgroups take
+// With up to two pairs per expert, on average over all of them, two kernels of dot
+// products, whose weights a wave reads in whole lines.  First the hidden layer: workgroups take
 // tiles of one expert's W1 and apply them to all its pairs.  Then the output:
 // workgroups own columns, for all experts, so that a sample's k terms meet in LDS
-// and are added in the order of its choices, without atomics.
+// and are added in the order of its choices, without atomics.  An expert's pairs go
+// through a tile two at a time, so ids that collapse onto one of many experts make
+// it as many reads of that expert from the caches (bfloat16 1024 -> 1024 -> 1024, 512
+// pairs over 256 experts 279 us, all of one 775).
 // With more pairs the vector units would take longer than the read, and a column's
 // owner would have too much of it: either layer goes through the matrix units, 16
-// pairs at a time, and a third kernel adds up the samples' terms.
+// pairs at a time, and a third kernel adds up the samples' terms.  There the pairs'
+// vectors, read again for every 16 rows of weights and three parts each in the
+// second bfloat16 layer, cost more than the weights.
 // Hidden values keep 24 bits between the kernels (rounding them to bfloat16 would
 // add an error as large as the output's own rounding, and saves only L2 traffic).
-// Measured: one sample through 2 of 16 experts 1024 -> 4096 -> 1024, bfloat16,
-// 11.6 us (33.6 MB, 2.9 TB/s); 16 samples through 4 of 64 gated experts of 1024, 60 us
-// (256 MB, 4.3 TB/s); 64 through 2 of 8 experts 1024 -> 4096 -> 1024, 69 us (134 MB).
+// Measured, weights from memory: one sample through 2 of 16 experts 1024 -> 4096 ->
+// 1024, bfloat16, 13.2 us (32.6 MB, 2.5 TB/s); 16 samples through 4 of 64 gated experts
+// of 1024, 66 us (256 MB, 3.9 TB/s); 64 through 2 of 8 experts 1024 -> 4096 -> 1024, 81 us
+// (134 MB; kernels of 5, 29, 47 and 5).
 #include <hip/hip_runtime.h>
 
 #include <cfloat>
@@ -186,9 +192,9 @@ __device__ __forceinline__ void dots(float (&acc)[R * M], const T* const (&w)[R]
     }
 }
 
-// Sums of N values (a power of two) over G lanes: while N halves, a lane keeps
-// one half of the values and hands over the other, so lane g ends up with value
-// g / (G / N).  (With fewer lanes than values it keeps N / G of them: not used.)
+// Sums of N values (a power of two, G at most) over G lanes: while N halves, a lane
+// keeps one half of the values and hands over the other, so lane g ends up with
+// value g / (G / N).
 template <int N, int G>
 __device__ __forceinline__ float sum_lanes(float (&v)[N], int g) {
     static_assert(N <= G, "a lane for every value");

@@ -1,5 +1,9 @@
 // How a call of the gated linear recurrence is cut up: host code, shared by the
-// launchers and the workspace sizes.
+// launchers and the workspace sizes.  It knows the sequences' average length only:
+// offsets are on the device.  Where one sequence is far longer than the average, a
+// lane or a workgroup walks it while the card idles (one of 30000 steps beside 10000
+// of up to one step, 4 channels: 4.9 ms, by itself 17 us; one of 32768 beside 300 of one
+// step, 64 channels: 644 us, by itself 16).
 #include "fields.hpp"
 
 namespace nerf {
